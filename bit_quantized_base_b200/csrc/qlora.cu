@@ -16,6 +16,7 @@
 #include "qlora_stream.cuh"
 #include "qlora_short.cuh"
 #include "qlora_w4a8.cuh"
+#include "qlora_norm.cuh"
 #include <algorithm>
 #include <utility>
 #include "qlora_quant.cuh"
@@ -386,13 +387,13 @@ enum Kind : int {
   kKindFusedFwd = 0, kKindFusedDx, kKindDownT, kKindDownU, kKindWgrad,
   kKindGFusedFwd, kKindGFusedDx, kKindGDownT, kKindGDownU, kKindGWgrad,
   kKindStreamFwd, kKindStreamDx, kKindStreamReduce, kKindShortFwd, kKindShortDx,
-  kKindW4a8Quant, kKindW4a8Gemm, kNumKinds
+  kKindW4a8Quant, kKindW4a8Gemm, kKindNormFwd, kKindNormBwd, kKindNormDgamma, kNumKinds
 };
 const char* const kKindNames[kNumKinds] = {
     "fused_fwd", "fused_dx", "lora_down_T", "lora_down_U", "lora_wgrad",
     "grouped_fused_fwd", "grouped_fused_dx", "grouped_lora_down_T", "grouped_lora_down_U",
     "grouped_lora_wgrad", "stream_fwd", "stream_dx", "stream_reduce", "short_fwd", "short_dx",
-    "w4a8_quant", "w4a8_gemm"};
+    "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma"};
 constexpr int kMaxProfiled = 65536;
 
 std::atomic<int64_t> g_launches{0};
@@ -1043,6 +1044,35 @@ qlora_status_t run_bwd(const qlora_weight_t* W, int E, const int32_t* offsets, b
   return launch_wgrad(X, dY, T, U, M, W->N, W->K, r, scale, dA, dB, ws, L, offsets, E, grouped, s);
 }
 
+// The W4A8 forward.  X_codes / X_scales: X already in MXFP8, or null to quantise it here (into the
+// workspace).
+qlora_status_t run_w4a8(const qlora_weight_t* W, const void* X, const void* X_codes,
+                        const void* X_scales, const void* A, const void* B, void* Y, void* T_save,
+                        int64_t M, int r, float scale, void* ws, size_t ws_bytes, cudaStream_t s) {
+  qlora_status_t st = check_common(W, M, r);
+  if (st != QLORA_OK) return st;
+  if (W->fmt != QLORA_FMT_MXFP4 || W->K % 128 != 0) return QLORA_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(W->codes) & 31u) != 0 || !act_ok(X, M) || !ptr_ok(A) ||
+      !ptr_ok(B) || !act_ok(Y, M) || (T_save && !aligned16(T_save)))
+    return QLORA_ERR_INVALID_ARG;
+  const W4a8Layout L = w4a8_layout(W->K, M, r);
+  if (!ws || !aligned16(ws) || ws_bytes < L.total) return QLORA_ERR_WORKSPACE;
+  if (M == 0) return QLORA_OK;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  void* T = T_save ? T_save : w + L.t;
+  if (!X_codes) {
+    st = launch_mxfp8_quant(X, M, W->K, w + L.xq, w + L.xs, s);
+    if (st != QLORA_OK) return st;
+    X_codes = w + L.xq;
+    X_scales = w + L.xs;
+  }
+  // T = X A^T from the bf16 X and Zs = bf16(s T), as in the bf16 forward
+  st = launch_lora_down(false, X, M, W->K, A, r, scale, nullptr, T, w + L.zs, ws_status(ws),
+                        nullptr, 1, false, kDownCtasBesidePair, s);
+  if (st != QLORA_OK) return st;
+  return launch_w4a8_gemm(W, X_codes, X_scales, w + L.zs, B, Y, M, r, ws_status(ws), s);
+}
+
 qlora_status_t check_groups(int E, const int32_t* d_offsets) {
   if (E < 1 || E > kMaxExperts) return QLORA_ERR_UNSUPPORTED;
   if (!d_offsets || (reinterpret_cast<uintptr_t>(d_offsets) & 3u) != 0) return QLORA_ERR_INVALID_ARG;
@@ -1051,6 +1081,8 @@ qlora_status_t check_groups(int E, const int32_t* d_offsets) {
 
 }  // namespace
 }  // namespace qlora
+
+#include "qlora_norm_host.cuh"
 
 extern "C" {
 
@@ -1070,28 +1102,21 @@ qlora_status_t qlora_mxfp8_quantize(const void* X, int64_t M, int64_t K, void* c
   return launch_mxfp8_quant(X, M, K, codes, scales, reinterpret_cast<cudaStream_t>(stream));
 }
 
+qlora_status_t qlora_linear_fwd_w4a8_codes(const qlora_weight_t* W, const void* X,
+                                           const void* X_codes, const void* X_scales,
+                                           const void* A, const void* B, void* Y, void* T_save,
+                                           int64_t M, int r, float scale, void* ws,
+                                           size_t ws_bytes, qlora_stream_t stream) {
+  if (M > 0 && (!ptr_ok(X_codes) || !ptr_ok(X_scales))) return QLORA_ERR_INVALID_ARG;
+  return run_w4a8(W, X, X_codes, X_scales, A, B, Y, T_save, M, r, scale, ws, ws_bytes,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
 qlora_status_t qlora_linear_fwd_w4a8(const qlora_weight_t* W, const void* X, const void* A,
                                      const void* B, void* Y, void* T_save, int64_t M, int r,
                                      float scale, void* ws, size_t ws_bytes, qlora_stream_t stream) {
-  qlora_status_t st = check_common(W, M, r);
-  if (st != QLORA_OK) return st;
-  if (W->fmt != QLORA_FMT_MXFP4 || W->K % 128 != 0) return QLORA_ERR_UNSUPPORTED;
-  if ((reinterpret_cast<uintptr_t>(W->codes) & 31u) != 0 || !act_ok(X, M) || !ptr_ok(A) ||
-      !ptr_ok(B) || !act_ok(Y, M) || (T_save && !aligned16(T_save)))
-    return QLORA_ERR_INVALID_ARG;
-  const W4a8Layout L = w4a8_layout(W->K, M, r);
-  if (!ws || !aligned16(ws) || ws_bytes < L.total) return QLORA_ERR_WORKSPACE;
-  if (M == 0) return QLORA_OK;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint8_t* w = static_cast<uint8_t*>(ws);
-  void* T = T_save ? T_save : w + L.t;
-  st = launch_mxfp8_quant(X, M, W->K, w + L.xq, w + L.xs, s);
-  if (st != QLORA_OK) return st;
-  // T = X A^T from the bf16 X and Zs = bf16(s T), as in the bf16 forward
-  st = launch_lora_down(false, X, M, W->K, A, r, scale, nullptr, T, w + L.zs, ws_status(ws),
-                        nullptr, 1, false, kDownCtasBesidePair, s);
-  if (st != QLORA_OK) return st;
-  return launch_w4a8_gemm(W, w + L.xq, w + L.xs, w + L.zs, B, Y, M, r, ws_status(ws), s);
+  return run_w4a8(W, X, nullptr, nullptr, A, B, Y, T_save, M, r, scale, ws, ws_bytes,
+                  reinterpret_cast<cudaStream_t>(stream));
 }
 
 qlora_status_t qlora_linear_fwd_noalloc(const qlora_weight_t* W, const void* X, const void* A,

@@ -52,12 +52,32 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
   return d;
 }
 
-// One 32-element block: the shared exponent e = clamp(floor(log2 amax) - 8 + 127, 0, 254) (8 is
-// E4M3's largest normal exponent; an all-zero block gets 0), elements the nearest E4M3 of
+// The E8M0 exponent of a block whose largest bf16 magnitude (its 15 low bits) is `amax`:
+// e = clamp(floor(log2 amax) - 8 + 127, 0, 254) (8 is E4M3's largest normal exponent; an all-zero
+// block gets 0).  floor(log2 amax) of a bf16 amax is its exponent field minus 127 (a subnormal or
+// zero amax clamps e to 0).
+__device__ __forceinline__ int mxfp8_exponent(uint32_t amax) {
+  const int e = int(amax >> 7) - 8;
+  return e < 0 ? 0 : (e > 254 ? 254 : e);
+}
+// 2^(127 - e): a normal binary32 for e <= 253, the subnormal 2^-127 for e = 254
+__device__ __forceinline__ float mxfp8_inverse(int e) {
+  return e <= 253 ? __uint_as_float(uint32_t(254 - e) << 23) : __uint_as_float(0x00400000u);
+}
+// Four bf16 elements (two words, the first element in the low half) as E4M3 codes of x * inv.
+__device__ __forceinline__ uint32_t mxfp8_encode4(uint32_t a, uint32_t c, float inv) {
+  const uint32_t lo = cvt_e4m3x2(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xFFFF0000u) * inv);
+  const uint32_t hi = cvt_e4m3x2(__uint_as_float(c << 16) * inv, __uint_as_float(c & 0xFFFF0000u) * inv);
+  const uint32_t v = lo | (hi << 16);
+  // a magnitude that rounded to zero keeps no sign: 0x80 -> 0x00 in every byte
+  const uint32_t mag0 = ((v & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & 0x80808080u;   // 0x80 where nonzero
+  return v & (mag0 | 0x7F7F7F7Fu);
+}
+
+// One 32-element block: the shared exponent (mxfp8_exponent), elements the nearest E4M3 of
 // x / 2^(e-127), ties to even, saturating at 448, a zero magnitude without its sign (the OCP MX
-// shared-exponent rule; the pages fix no rule of their own).  floor(log2 amax) of a bf16 amax is
-// its exponent field minus 127 (a subnormal or zero amax clamps e to 0), and x / 2^(e-127) is a
-// multiplication by an exact power of two, so the decision matches the fp64 definition.
+// shared-exponent rule; the pages fix no rule of their own).  x / 2^(e-127) is a multiplication
+// by an exact power of two, so the decision matches the fp64 definition.
 __global__ void __launch_bounds__(256) qlora_mxfp8_quant_kernel(const __grid_constant__ Mxfp8Params p) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -73,22 +93,11 @@ __global__ void __launch_bounds__(256) qlora_mxfp8_quant_kernel(const __grid_con
   uint32_t amax = 0;                 // bf16 magnitudes order as integers
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = max(amax, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-  int e = int(amax >> 7) - 8;
-  e = e < 0 ? 0 : (e > 254 ? 254 : e);
-  // 2^(127 - e): a normal binary32 for e <= 253, the subnormal 2^-127 for e = 254
-  const float inv = e <= 253 ? __uint_as_float(uint32_t(254 - e) << 23) : __uint_as_float(0x00400000u);
+  const int e = mxfp8_exponent(amax);
+  const float inv = mxfp8_inverse(e);
   uint32_t out[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t a = w[2 * i], c = w[2 * i + 1];
-    const uint32_t lo = cvt_e4m3x2(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xFFFF0000u) * inv);
-    const uint32_t hi = cvt_e4m3x2(__uint_as_float(c << 16) * inv, __uint_as_float(c & 0xFFFF0000u) * inv);
-    uint32_t v = lo | (hi << 16);
-    // a magnitude that rounded to zero keeps no sign: 0x80 -> 0x00 in every byte
-    const uint32_t mag0 = ((v & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & 0x80808080u;   // 0x80 where nonzero
-    v &= mag0 | 0x7F7F7F7Fu;
-    out[i] = v;
-  }
+  for (int i = 0; i < 8; ++i) out[i] = mxfp8_encode4(w[2 * i], w[2 * i + 1], inv);
   uint4* dst = reinterpret_cast<uint4*>(p.codes + b * 32);
   dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
   dst[1] = make_uint4(out[4], out[5], out[6], out[7]);

@@ -32,7 +32,8 @@ EXPORTS = ("qlora_workspace_size", "qlora_workspace_init", "qlora_linear_fwd", "
            "qlora_profile_reset", "qlora_profile_read", "qlora_linear_fwd_noalloc",
            "qlora_linear_fwd_noalloc_status", "qlora_linear_fwd_w4a8", "qlora_mxfp8_quantize",
            "qlora_debug_decode_rate", "qlora_quantize", "qlora_merge_requantize",
-           "qlora_loftq_workspace_size", "qlora_loftq")
+           "qlora_loftq_workspace_size", "qlora_loftq", "qlora_linear_fwd_w4a8_codes",
+           "qlora_rmsnorm_fwd", "qlora_rmsnorm_workspace_size", "qlora_rmsnorm_bwd")
 
 
 class QLoraError(RuntimeError):
@@ -83,6 +84,13 @@ def _load():
     L.qlora_launch_count.restype = c.c_int64
     L.qlora_linear_fwd_w4a8.argtypes = [W, P, P, P, P, P, c.c_int64, c.c_int, c.c_float, P,
                                         c.c_size_t, P]
+    L.qlora_linear_fwd_w4a8_codes.argtypes = [W, P, P, P, P, P, P, P, c.c_int64, c.c_int, c.c_float,
+                                              P, c.c_size_t, P]
+    L.qlora_rmsnorm_fwd.argtypes = [P, P, P, c.c_float, P, P, P, P, P, c.c_int64, c.c_int64, P]
+    L.qlora_rmsnorm_workspace_size.argtypes = [c.c_int64, c.c_int64]
+    L.qlora_rmsnorm_workspace_size.restype = c.c_size_t
+    L.qlora_rmsnorm_bwd.argtypes = [P, P, P, c.c_float, P, P, P, P, c.c_int64, c.c_int64, P,
+                                    c.c_size_t, P]
     L.qlora_mxfp8_quantize.argtypes = [P, c.c_int64, c.c_int64, P, P, P]
     L.qlora_linear_fwd_noalloc.argtypes = [W, P, P, P, P, P, c.c_int64, c.c_int, c.c_float, P]
     L.qlora_linear_fwd_noalloc.restype = c.c_int
@@ -95,7 +103,8 @@ def _load():
                  "qlora_grouped_fwd", "qlora_grouped_bwd", "qlora_get_device_status",
                  "qlora_debug_dequant", "qlora_debug_wait_timeout", "qlora_debug_decode_rate",
                  "qlora_quantize", "qlora_merge_requantize", "qlora_loftq",
-                 "qlora_linear_fwd_w4a8", "qlora_mxfp8_quantize",
+                 "qlora_linear_fwd_w4a8", "qlora_mxfp8_quantize", "qlora_linear_fwd_w4a8_codes",
+                 "qlora_rmsnorm_fwd", "qlora_rmsnorm_bwd",
                  "qlora_profile_enable",
                  "qlora_profile_reset", "qlora_profile_read"):
         getattr(L, name).restype = c.c_int
@@ -125,6 +134,34 @@ def _p(t):
 def _stream(stream):
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _args(where, *specs):
+    """Check the tensors of one call and return (device, *pointers).  A spec is (name, tensor, dtype,
+    elements, required); a tensor must be contiguous, of that dtype and element count, and on the
+    current CUDA device, whose current stream the call is enqueued on (-1 elements: any count)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    out = [dev]
+    for name, t, dtype, n, required in specs:
+        if t is None:
+            if required:
+                raise QLoraError(1, f"{where}: {name} is required")
+            out.append(None)
+            continue
+        if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or \
+                (n >= 0 and t.numel() != n):
+            raise QLoraError(1, f"{where}: {name} must be a contiguous {dtype} tensor of {n} elements "
+                                f"on the current CUDA device, got {tuple(t.shape)} {t.dtype} on "
+                                f"{t.device} (current device {dev})")
+        out.append(t.data_ptr())
+    return out
+
+
+def _on(stream, dev):
+    """The raw handle of `stream`, or of the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -171,6 +208,48 @@ def qlora_linear_fwd_w4a8(W: Weight, X, A, B, Y, T_save, M, r, scale, ws, stream
     _check(lib.qlora_linear_fwd_w4a8(W.ref, _p(X), _p(A), _p(B), _p(Y), _p(T_save), int(M), int(r),
                                      float(scale), _p(ws), 0 if ws is None else ws.numel(),
                                      _stream(stream)), "qlora_linear_fwd_w4a8")
+
+
+def qlora_linear_fwd_w4a8_codes(W: Weight, X, X_codes, X_scales, A, B, Y, T_save, M, r, scale, ws,
+                                stream=None):
+    """qlora_linear_fwd_w4a8 with X already in MXFP8 (X_codes [M,K], X_scales [M,K/32] uint8)."""
+    N, K = W.N, W.K
+    bf, u8 = torch.bfloat16, torch.uint8
+    dev, x, xc, xs, a, b, y, t, w = _args(
+        "qlora_linear_fwd_w4a8_codes", ("X", X, bf, M * K, M > 0), ("X_codes", X_codes, u8, M * K, M > 0),
+        ("X_scales", X_scales, u8, M * K // 32, M > 0), ("A", A, bf, r * K, True),
+        ("B", B, bf, N * r, True), ("Y", Y, bf, M * N, M > 0), ("T_save", T_save, bf, M * r, False),
+        ("ws", ws, u8, -1, False))
+    _check(lib.qlora_linear_fwd_w4a8_codes(W.ref, x, xc, xs, a, b, y, t, int(M), int(r), float(scale), w,
+                                           0 if ws is None else ws.numel(), _on(stream, dev)),
+           "qlora_linear_fwd_w4a8_codes")
+
+
+def qlora_rmsnorm_fwd(X, R, gamma, eps, S, Y, codes, scales, rstd, M, K, stream=None):
+    """S = X + R, Y = S / rms(S) * gamma, as bf16 (Y) and / or MXFP8 (codes, scales).  R, gamma, S,
+    Y, codes + scales and rstd may be None."""
+    n, bf, u8 = M * K, torch.bfloat16, torch.uint8
+    dev, x, r, g, s, y, c, sc, rs = _args(
+        "qlora_rmsnorm_fwd", ("X", X, bf, n, M > 0), ("R", R, bf, n, False), ("gamma", gamma, bf, K, False),
+        ("S", S, bf, n, False), ("Y", Y, bf, n, False), ("codes", codes, u8, n, False),
+        ("scales", scales, u8, n // 32, False), ("rstd", rstd, torch.float32, M, False))
+    _check(lib.qlora_rmsnorm_fwd(x, r, g, eps, s, y, c, sc, rs, M, K, _on(stream, dev)), "qlora_rmsnorm_fwd")
+
+
+def qlora_rmsnorm_workspace_size(M, K):
+    return int(lib.qlora_rmsnorm_workspace_size(int(M), int(K)))
+
+
+def qlora_rmsnorm_bwd(S, rstd, gamma, eps, dY, dS_in, dS, dgamma, M, K, ws=None, stream=None):
+    """Gradients of qlora_rmsnorm_fwd: dS (of X and of R) and, unless None, dgamma.  rstd None is
+    recomputed from S and eps; dS_in None is zero; ws is needed with dgamma only."""
+    n, bf = M * K, torch.bfloat16
+    dev, s, rs, g, dy, di, ds, dg, w = _args(
+        "qlora_rmsnorm_bwd", ("S", S, bf, n, M > 0), ("rstd", rstd, torch.float32, M, False),
+        ("gamma", gamma, bf, K, False), ("dY", dY, bf, n, M > 0), ("dS_in", dS_in, bf, n, False),
+        ("dS", dS, bf, n, M > 0), ("dgamma", dgamma, bf, K, False), ("ws", ws, torch.uint8, -1, False))
+    _check(lib.qlora_rmsnorm_bwd(s, rs, g, eps, dy, di, ds, dg, M, K, w, 0 if ws is None else ws.numel(),
+                                 _on(stream, dev)), "qlora_rmsnorm_bwd")
 
 
 def qlora_mxfp8_quantize(X, M, K, codes, scales, stream=None):

@@ -235,6 +235,55 @@ QLORA_API qlora_status_t qlora_linear_fwd_w4a8(const qlora_weight_t* W, const vo
 QLORA_API qlora_status_t qlora_mxfp8_quantize(const void* X, int64_t M, int64_t K, void* codes,
                                               void* scales, qlora_stream_t stream);
 
+/* qlora_linear_fwd_w4a8 with X already in MXFP8: X_codes [M,K] and X_scales [M,K/32] as
+ * qlora_mxfp8_quantize or qlora_rmsnorm_fwd write them (from the same bf16 X, which the LoRA path
+ * reads).  Bitwise the result of qlora_linear_fwd_w4a8, one launch less.  Same limits, workspace
+ * and errors; X_codes and X_scales 16-byte aligned (with M == 0 they may be NULL). */
+QLORA_API qlora_status_t qlora_linear_fwd_w4a8_codes(const qlora_weight_t* W, const void* X,
+                                                     const void* X_codes, const void* X_scales,
+                                                     const void* A, const void* B, void* Y,
+                                                     void* T_save, int64_t M, int r, float scale,
+                                                     void* ws, size_t ws_bytes,
+                                                     qlora_stream_t stream);
+
+/* RMS norm with the residual's addition, in front of a block of projections:
+ *   S = bf16(X + R)      rstd[m] = 1 / sqrt(mean_k S[m,k]^2 + eps)      Y = bf16(S rstd gamma)
+ * The norm is taken of the stored S (rounded once, the addition in binary32), so a backward pass
+ * that reads S sees the numbers the forward normalised.  R NULL: S is X itself.
+ *   X, R [M,K] bf16 (R NULL or given); gamma [K] bf16 or NULL (all ones);
+ *   S [M,K] bf16 out or NULL (only with R); may be the same buffer as X or R;
+ *   Y [M,K] bf16 out or NULL; may be the same buffer as X or R (not as S);
+ *   codes [M,K] uint8 and scales [M,K/32] uint8 out, both or neither: Y in MXFP8, bit for bit what
+ *     qlora_mxfp8_quantize makes of Y (written or not) -- the input of qlora_linear_fwd_w4a8_codes;
+ *   rstd [M] fp32 out or NULL, for the backward pass.  At least one of Y and codes is required.
+ * The squares are summed in at most 32 binary32 terms per thread and then in binary64; with codes
+ * the products S rstd gamma carry their rounding errors, so Y is the definition's value rounded
+ * once and a code next to a rounding border does not depend on the order of operations.
+ * Limits: K % 8 == 0 (K % 32 == 0 with codes), 8 <= K <= 32768 (larger: QLORA_ERR_UNSUPPORTED),
+ * M >= 0 (0 is a no-op), eps finite and >= 0, every pointer 16-byte aligned.  One launch. */
+QLORA_API qlora_status_t qlora_rmsnorm_fwd(const void* X, const void* R, const void* gamma,
+                                           float eps, void* S, void* Y, void* codes, void* scales,
+                                           float* rstd, int64_t M, int64_t K,
+                                           qlora_stream_t stream);
+
+/* Backward of qlora_rmsnorm_fwd.  With v = gamma dY:
+ *   dS = dS_in + rstd (v - S rstd^2 mean_k(v S))        dgamma[k] = sum_m dY[m,k] S[m,k] rstd[m]
+ * dS is the gradient of X and of R alike.
+ *   S [M,K] bf16: the forward's S (its X when R was NULL); rstd [M] fp32 or NULL (recomputed from S
+ *   and eps; eps is read only then); gamma as in the forward; dY [M,K] bf16; dS_in [M,K] bf16 or
+ *   NULL: the gradient that reaches S by the residual path;
+ *   dS [M,K] bf16 out; may be the same buffer as dY, dS_in or S;
+ *   dgamma [K] bf16 out or NULL (a frozen gamma); overwritten (zeros for M == 0).
+ *   ws: device scratch of qlora_rmsnorm_workspace_size(M, K) bytes, 16-byte aligned, needed only
+ *   with dgamma (else it may be NULL); needs no initialisation.
+ * dgamma is summed in binary32 in a fixed order.  Limits as qlora_rmsnorm_fwd.  One launch, two
+ * with dgamma. */
+QLORA_API size_t qlora_rmsnorm_workspace_size(int64_t M, int64_t K);
+QLORA_API qlora_status_t qlora_rmsnorm_bwd(const void* S, const float* rstd, const void* gamma,
+                                           float eps, const void* dY, const void* dS_in, void* dS,
+                                           void* dgamma, int64_t M, int64_t K, void* ws,
+                                           size_t ws_bytes, qlora_stream_t stream);
+
 /* Synchronise `stream` and read the status word of qlora_linear_fwd_noalloc's fixed scratch on
  * the current device: QLORA_OK, or the device-side error of the last no-alloc call (each call
  * clears it when it starts).  Allocates nothing.  Not for the compute path. */
@@ -339,7 +388,7 @@ QLORA_API qlora_status_t qlora_debug_decode_rate(int fmt, int iters,
  * returns, per kernel kind, the launch count and total milliseconds.  Kinds: "fused_fwd",
  * "fused_dx", "lora_down_T", "lora_down_U", "lora_wgrad" (grouped variants add "grouped_"),
  * "stream_fwd", "stream_dx", "stream_reduce" (batches of 65-256 rows), "short_fwd", "short_dx"
- * (batches of up to 64 rows).
+ * (batches of up to 64 rows), "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma".
  * Host-side bookkeeping only; the compute path is unchanged when profiling is off. */
 QLORA_API int64_t qlora_launch_count(void);
 QLORA_API qlora_status_t qlora_profile_enable(int enable);
