@@ -17,6 +17,7 @@
 #include "qlora_short.cuh"
 #include "qlora_w4a8.cuh"
 #include "qlora_norm.cuh"
+#include "qlora_act_down.cuh"
 #include <algorithm>
 #include <utility>
 #include "qlora_quant.cuh"
@@ -387,13 +388,15 @@ enum Kind : int {
   kKindFusedFwd = 0, kKindFusedDx, kKindDownT, kKindDownU, kKindWgrad,
   kKindGFusedFwd, kKindGFusedDx, kKindGDownT, kKindGDownU, kKindGWgrad,
   kKindStreamFwd, kKindStreamDx, kKindStreamReduce, kKindShortFwd, kKindShortDx,
-  kKindW4a8Quant, kKindW4a8Gemm, kKindNormFwd, kKindNormBwd, kKindNormDgamma, kNumKinds
+  kKindW4a8Quant, kKindW4a8Gemm, kKindNormFwd, kKindNormBwd, kKindNormDgamma,
+  kKindGatedFwd, kKindGatedDx, kKindActFwd, kKindActDown, kKindBiasSum, kNumKinds
 };
 const char* const kKindNames[kNumKinds] = {
     "fused_fwd", "fused_dx", "lora_down_T", "lora_down_U", "lora_wgrad",
     "grouped_fused_fwd", "grouped_fused_dx", "grouped_lora_down_T", "grouped_lora_down_U",
     "grouped_lora_wgrad", "stream_fwd", "stream_dx", "stream_reduce", "short_fwd", "short_dx",
-    "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma"};
+    "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma",
+    "gated_fwd", "gated_dx", "act_fwd", "act_down", "bias_sum"};
 constexpr int kMaxProfiled = 65536;
 
 std::atomic<int64_t> g_launches{0};
@@ -446,7 +449,7 @@ qlora_status_t launch_lora_down(bool r_mn, const void* act, int64_t M, int64_t K
                                 int r, float s, const float* ts, void* z, void* zs, int* status,
                                 const int32_t* offsets, int E, bool grouped, int max_ctas,
                                 cudaStream_t st, float zs_mul = 1.0f, int wide = 0,
-                                void* sums = nullptr, void* header = nullptr) {
+                                void* sums = nullptr, void* header = nullptr, int ldzs = 0) {
   DownParams p{};
   const int rpad = rank_pad(r);
   const DownPlan dp = down_plan(M, Kc, E, max_ctas > 0 ? max_ctas : num_sms(),
@@ -475,6 +478,7 @@ qlora_status_t launch_lora_down(bool r_mn, const void* act, int64_t M, int64_t K
   p.E = E;
   p.s = s;
   p.zs_mul = zs_mul;
+  p.ldzs = ldzs > 0 ? ldzs : r;
   if (dp.C > 1) {
     p.cpart = static_cast<float*>(sums);
     p.ccount = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(header) + kDownCountOffset);
@@ -726,8 +730,8 @@ qlora_status_t launch_short(const qlora_weight_t* W, bool dx, const void* act, c
 // dB [E, N, r] = s dY_e^T T_e and dA [E, r, K] = s U_e^T X_e over each expert's rows.
 qlora_status_t launch_wgrad(const void* X, const void* dY, const void* T, const void* U, int64_t M,
                             int64_t N, int64_t K, int r, float s, void* dA, void* dB, void* ws,
-                            const WsLayout& L, const int32_t* offsets, int E, bool grouped,
-                            cudaStream_t st) {
+                            const int32_t* offsets, int E, bool grouped, cudaStream_t st,
+                            const float* dy_mul = nullptr, const float* dy_div = nullptr) {
   WgradParams p{};
   const int rpad = rank_pad(r);
   const WgradPlan wp = wgrad_plan(N, K, M, E, num_sms());
@@ -756,6 +760,8 @@ qlora_status_t launch_wgrad(const void* X, const void* dY, const void* T, const 
   p.tiles1 = wp.tiles1;
   p.E = E;
   p.s = s;
+  p.l0_mul = dy_mul;
+  p.l0_div = dy_div;
   const size_t smem = lora::smem_bytes(E);
   if (!set_smem(qlora_lora_wgrad_kernel, smem)) return QLORA_ERR_CUDA;
   const unsigned grid = unsigned(int64_t(E) * (wp.tiles0 + wp.tiles1) * wp.S);
@@ -905,11 +911,14 @@ qlora_status_t launch_w4a8_gemm(const qlora_weight_t* W, const void* xq, const v
 
 using namespace qlora;
 
+#include "qlora_mlp_layout.cuh"
+
 extern "C" {
 
 size_t qlora_workspace_size(int op, const qlora_weight_t* W, int64_t M, int r, int E) {
   if (check_weight(W) != QLORA_OK || M < 0 || !rank_ok(r)) return 0;
   if (op == QLORA_OP_FWD_W4A8) return w4a8_layout(W->K, M, r).total;
+  if (op >= QLORA_OP_GATED_MLP_FWD && op <= QLORA_OP_ACT_BWD) return mlp_workspace(op, W, M, r);
   const bool grouped = op == QLORA_OP_GROUPED_FWD || op == QLORA_OP_GROUPED_BWD;
   if (!grouped && op != QLORA_OP_FWD && op != QLORA_OP_BWD) return 0;
   if (grouped && (E < 1 || E > kMaxExperts)) return 0;
@@ -1028,7 +1037,7 @@ qlora_status_t run_bwd(const qlora_weight_t* W, int E, const int32_t* offsets, b
       if (cudaEventRecord(side->fork[slot], s) != cudaSuccess ||
           cudaStreamWaitEvent(side->stream, side->fork[slot], 0) != cudaSuccess)
         return QLORA_ERR_CUDA;
-      st = launch_wgrad(X, dY, T, U, M, W->N, W->K, r, scale, dA, dB, ws, L, offsets, E, grouped,
+      st = launch_wgrad(X, dY, T, U, M, W->N, W->K, r, scale, dA, dB, ws, offsets, E, grouped,
                         side->stream);
       if (st != QLORA_OK) return st;
       if (cudaEventRecord(side->join[slot], side->stream) != cudaSuccess) return QLORA_ERR_CUDA;
@@ -1041,7 +1050,7 @@ qlora_status_t run_bwd(const qlora_weight_t* W, int E, const int32_t* offsets, b
     st = run_dx();
     if (st != QLORA_OK) return st;
   }
-  return launch_wgrad(X, dY, T, U, M, W->N, W->K, r, scale, dA, dB, ws, L, offsets, E, grouped, s);
+  return launch_wgrad(X, dY, T, U, M, W->N, W->K, r, scale, dA, dB, ws, offsets, E, grouped, s);
 }
 
 // The W4A8 forward.  X_codes / X_scales: X already in MXFP8, or null to quantise it here (into the
@@ -1083,6 +1092,7 @@ qlora_status_t check_groups(int E, const int32_t* d_offsets) {
 }  // namespace qlora
 
 #include "qlora_norm_host.cuh"
+#include "qlora_mlp_host.cuh"
 
 extern "C" {
 

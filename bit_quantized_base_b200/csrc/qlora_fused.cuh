@@ -45,11 +45,27 @@
 // The weight tile is K-major for the forward pass (rows of W are rows of the operand) and
 // MN-major for dX (rows of W run along the contraction); in both cases a 64-element item is one
 // 128-byte swizzled row, so the decode stage is the same code.
+//
+// Variants (template argument EPI):
+//   kEpiAct    forward only:  Y = act(Z) + residual with Z = the product above + bias; Z may be
+//              saved.  Only the epilogue differs.
+//   kEpiGated  forward: H = act(G) * U, two weights in one tile: CTA rank 0 decodes 128 rows of the
+//              gate weight and rank 1 the same 128 rows of the up weight, so each CTA's
+//              accumulator holds 128 columns of G and the same 128 columns of U for its own rows,
+//              and the epilogue multiplies them without leaving registers (G and U never go to
+//              memory unless they are to be saved).
+//              dX: dX = dG deq(Wg) + dU deq(Wu) + s (dG Bg) Ag + s (dU Bu) Au, one contraction over
+//              the rows of both weights one after the other, into one accumulator.
+//              The LoRA steps contract the concatenated rank 2r (one 64-deep step, two for r = 64):
+//              Zs [M, 2r] holds both scaled Z, and the weight operand's other half is zero.
+//              NVFP4: the two tensor scales multiply their halves of the forward's accumulator;
+//              dX has one accumulator, so dU arrives multiplied by ts_up / ts_gate.
 #pragma once
 #include <cuda_bf16.h>
 #include "qlora_ptx.cuh"
 #include "qlora_dequant.cuh"
 #include "qlora_groups.cuh"
+#include "qlora_act.cuh"
 
 namespace qlora {
 namespace fused {
@@ -91,6 +107,26 @@ struct FusedParams {
   int tail_split;                    // the last tail_split 512-row tiles run as 2 x 256-row tiles
   uint32_t zero;                     // 0 (see zero_after)
 };
+
+enum : int { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2 };
+
+// What the act and gated variants take besides.  Gated: the members above describe the gate weight
+// (tm_act: X or dG; tm_zs: Zs [M, 2r]), these the up weight.
+struct FusedExParams : FusedParams {
+  CUtensorMap tm_act_up;             // gated dX: dU
+  CUtensorMap tm_codes_up;
+  const void* scales_up;
+  const float* scales2_up;
+  const float* tensor_scale_up;
+  const __nv_bfloat16* lora_up_up;   // gated: Bu (forward), Au (dX)
+  const __nv_bfloat16 *bias, *residual;   // act: [N], [M, N], or null
+  __nv_bfloat16 *save0, *save1;      // act: Z; gated: G and U; or null
+  int act;                           // Act
+};
+template <int EPI>
+struct FusedParamsOf { using type = FusedExParams; };
+template <>
+struct FusedParamsOf<kEpiPlain> { using type = FusedParams; };
 
 // Tile t of an expert's (m-tile, n-tile) grid, in raster groups of `group_m` m-tiles.  The
 // forward takes groups of GM: a wave then shares each weight tile among several row blocks.  dX
@@ -221,10 +257,14 @@ struct ItemGeom {
   }
 };
 
-template <int FMT, bool DX>
+template <int FMT, bool DX, int EPI = kEpiPlain>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fused::kThreads, 1)
-qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
+qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::type p) {
   using namespace fused;
+  static_assert(!(DX && EPI == kEpiAct), "the act epilogue is a forward one");
+  constexpr bool GATED = EPI == kEpiGated;
+  constexpr bool DUAL = GATED && DX;           // contraction over both weights' rows
+  constexpr int TN = GATED && !DX ? HN : BN;   // output columns of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -277,7 +317,10 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
     ptx::prefetch_tmap(&p.tm_act);
     ptx::prefetch_tmap(&p.tm_zs);
   }
-  if (warp == kCodeWarp && lane == 0) ptx::prefetch_tmap(&p.tm_codes);
+  if (warp == kCodeWarp && lane == 0) {
+    ptx::prefetch_tmap(&p.tm_codes);
+    if constexpr (GATED) ptx::prefetch_tmap(&p.tm_codes_up);
+  }
   if (warp == kMmaWarp) {
     ptx::tmem_alloc_pair(ptx::smem_u32(tmem_slot), kTmemCols);
     ptx::tmem_relinquish_pair();
@@ -296,7 +339,9 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
   ptx::griddep_launch_dependents();
 
   const int num_tiles = grp_view.total() + p.tail_split;
-  const int nk = p.num_k;
+  const int nk1 = p.num_k;                                // contraction steps of one weight
+  const int nk = DUAL ? 2 * nk1 : nk1;                    // of the tile, before its LoRA steps
+  const int nt = GATED ? nk + (2 * p.r + BK - 1) / BK : nk + 1;   // all steps of the tile
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------------ activation producer
@@ -307,7 +352,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
         const PairTile pt = pair_tile_at<DX>(grp_view, t, p.num_n, p.tail_split);
         const int m0 = pt.row0 + int(rank) * HM;      // this CTA's rows of block 0 (+256: block 1)
         bool ok = true;
-        for (int ks = 0; ks <= nk; ++ks, ++i) {
+        for (int ks = 0; ks < nt; ++ks, ++i) {
           const uint32_t sx = i % NS, px = (i / NS) & 1u;
           if (!ptx::mbar_wait(empty_s(sx), px ^ 1u, p.status, abort_flag)) { ok = false; break; }
           if (ks == nk && !waited) {
@@ -319,10 +364,15 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
           for (int blk = 0; blk < pt.nb; ++blk) {
             const uint32_t xd = ptx::smem_u32(xs + (sx * MB + blk) * X_BYTES);
             if (ks < nk) {
-              if (ptx::dcheck(ptx::tma_x_ok(ks * BK, 2), p.status))
-                ptx::tma_load_2d_pair(xd, &p.tm_act, fx, ks * BK, m0 + blk * 2 * HM);
+              const CUtensorMap* tm = &p.tm_act;
+              int x = ks * BK;
+              if constexpr (DUAL) {
+                if (ks >= nk1) { tm = &p.tm_act_up; x = (ks - nk1) * BK; }
+              }
+              if (ptx::dcheck(ptx::tma_x_ok(x, 2), p.status))
+                ptx::tma_load_2d_pair(xd, tm, fx, x, m0 + blk * 2 * HM);
             } else {
-              ptx::tma_load_2d_pair(xd, &p.tm_zs, fx, 0, m0 + blk * 2 * HM);
+              ptx::tma_load_2d_pair(xd, &p.tm_zs, fx, GATED ? (ks - nk) * BK : 0, m0 + blk * 2 * HM);
             }
           }
         }
@@ -335,7 +385,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
       uint32_t j = 0;
       for (int t = pair; t < num_tiles; t += npairs) {
         const PairTile pt = pair_tile_at<DX>(grp_view, t, p.num_n, p.tail_split);
-        const int h0 = pt.nt * BN + int(rank) * HN;   // this CTA's weight half
+        const int h0 = pt.nt * TN + (TN == BN ? int(rank) * HN : 0);   // this CTA's weight half
         const int wrow0 = pt.e * p.N;                 // the expert's first row of the codes
         bool ok = true;
         for (int ks = 0; ks < nk; ++ks, ++j) {
@@ -345,8 +395,15 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
           const uint32_t cd = ptx::smem_u32(cs + sc * C_BYTES);
           const int cx = !DX ? ks * (BK / 2) : h0 / 2;
           if (!ptx::dcheck(ptx::tma_x_ok(cx, 1) && pt.e < p.E, p.status)) continue;
-          if (!DX) ptx::tma_load_2d(cd, &p.tm_codes, full_c(sc), cx, wrow0 + h0);
-          else ptx::tma_load_2d(cd, &p.tm_codes, full_c(sc), cx, wrow0 + ks * BK);
+          const CUtensorMap* tm = &p.tm_codes;
+          int kr = ks;
+          if constexpr (DUAL) {
+            if (ks >= nk1) { tm = &p.tm_codes_up; kr = ks - nk1; }
+          } else if constexpr (GATED) {
+            if (rank != 0) tm = &p.tm_codes_up;
+          }
+          if (!DX) ptx::tma_load_2d(cd, tm, full_c(sc), cx, wrow0 + h0);
+          else ptx::tma_load_2d(cd, tm, full_c(sc), cx, wrow0 + kr * BK);
         }
         if (!ok) break;
       }
@@ -372,7 +429,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
         if (!ptx::mbar_wait_cluster(acc_empty, (tc & 1u) ^ 1u, p.status, abort_flag)) break;
         ptx::tc_fence_after();
         bool ok = true;
-        for (int ks = 0; ks <= nk; ++ks, ++i) {
+        for (int ks = 0; ks < nt; ++ks, ++i) {
           const uint32_t st = i & (NS - 1);
           if (!ptx::mbar_wait_cluster(full_s(st), (i / NS) & 1u, p.status, abort_flag)) { ok = false; break; }
           ptx::tc_fence_after();
@@ -391,7 +448,8 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
                 ptx::mma_bf16_pair(tmem, a + kk * kAkk, b + kk * kBkk, idesc, kk ? 1u : acc0);
             }
           } else {
-            for (int kk = 0; kk < lora_kk; ++kk) {
+            const int kks = GATED ? min(BK / 16, (2 * p.r - (ks - nk) * BK) / 16) : lora_kk;
+            for (int kk = 0; kk < kks; ++kk) {
               ptx::mma_bf16_pair(tmem, a + kk * kAkk, b + kk * kBkk, idesc, 1u);
               if (nb == 2) ptx::mma_bf16_pair(tmem + BN, a + kABlk + kk * kAkk, b + kk * kBkk, idesc, 1u);
             }
@@ -407,7 +465,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
       uint32_t i = 0;
       for (int t = pair; t < num_tiles; t += npairs) {
         bool ok = true;
-        for (int ks = 0; ks <= nk; ++ks, ++i) {
+        for (int ks = 0; ks < nt; ++ks, ++i) {
           const uint32_t st = i % NS;
           if (!ptx::mbar_wait(full_s(st), (i / NS) & 1u, p.status, abort_flag)) { ok = false; break; }
           ptx::mbar_arrive_remote(full_leader0 + 8u * st);
@@ -431,8 +489,10 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
     uint32_t tc = 0;
     for (int t = pair; t < num_tiles; t += npairs, ++tc) {
       const PairTile pt = pair_tile_at<DX>(grp_view, t, p.num_n, p.tail_split);
-      const int c0 = pt.nt * BN;
+      const int c0 = pt.nt * TN;
       const float ts = (FMT == kFmtNVFP4 && p.tensor_scale) ? __ldg(p.tensor_scale + pt.e) : 1.0f;
+      float ts_up = 1.0f;
+      if constexpr (GATED && !DX && FMT == kFmtNVFP4) ts_up = __ldg(p.tensor_scale_up);
       if (!ptx::mbar_wait(acc_full, tc & 1u, p.status, abort_flag)) break;
       ptx::tc_fence_after();
 #pragma unroll 1
@@ -440,22 +500,13 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
         const int rbase = pt.row0 + blk * 2 * HM + int(rank) * HM + q * 32;
         if (rbase >= pt.row_end) continue;   // warp-uniform
         const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + uint32_t(blk * BN);
-#pragma unroll 1
-        for (int cb = 0; cb < BN / 32; ++cb) {
-          uint32_t v[32];
-          ptx::tmem_ld_32x32b_x32(tb + uint32_t(cb) * 32u, v);
-          ptx::tmem_ld_wait(v);
+        // One 32 x 32 block of this warp's rows (row = lane, `w` its 32 columns as bf16 pairs)
+        // through the staging tile to columns col0 .. col0+31 of `out`.
+        auto store_block = [&](const uint32_t (&w)[16], __nv_bfloat16* out, int col0) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float lo = __uint_as_float(v[g * 8 + 2 * j]), hi = __uint_as_float(v[g * 8 + 2 * j + 1]);
-              if constexpr (FMT == kFmtNVFP4) { lo *= ts; hi *= ts; }
-              w[j] = ptx::cvt_bf16x2(lo, hi);
-            }
-            ptx::st_shared_v4(stg + uint32_t(lane) * 64u + ((uint32_t(g) ^ wsw) << 4), w[0], w[1], w[2], w[3]);
-          }
+          for (int g = 0; g < 4; ++g)
+            ptx::st_shared_v4(stg + uint32_t(lane) * 64u + ((uint32_t(g) ^ wsw) << 4), w[4 * g], w[4 * g + 1],
+                              w[4 * g + 2], w[4 * g + 3]);
           __syncwarp();
           uint4 o[4];
 #pragma unroll
@@ -464,13 +515,76 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
             o[it] = ptx::ld_shared_v4(stg + rr * 64u + ((uint32_t(rc) ^ ((rr >> 1) & 3u)) << 4));
           }
           __syncwarp();
-          const int col = c0 + cb * 32 + rc * 8;
+          const int col = col0 + rc * 8;
 #pragma unroll
           for (int it = 0; it < 4; ++it) {
             const int row = rbase + it * 8 + rr0;
             if (row < pt.row_end && col < ncols && ptx::dcheck(row >= 0 && pt.row_end <= p.M, p.status))
-              *reinterpret_cast<uint4*>(p.out + size_t(row) * ncols + col) = o[it];
+              *reinterpret_cast<uint4*>(out + size_t(row) * ncols + col) = o[it];
           }
+        };
+#pragma unroll 1
+        for (int cb = 0; cb < TN / 32; ++cb) {
+          uint32_t v[32], w[16];
+          ptx::tmem_ld_32x32b_x32(tb + uint32_t(cb) * 32u, v);
+          ptx::tmem_ld_wait(v);
+          if constexpr (FMT == kFmtNVFP4) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * ts);
+          }
+          if constexpr (GATED && !DX) {
+            uint32_t u[32];
+            ptx::tmem_ld_32x32b_x32(tb + uint32_t(HN + cb * 32), u);
+            ptx::tmem_ld_wait(u);
+            if constexpr (FMT == kFmtNVFP4) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * ts_up);
+            }
+            if (p.save0) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = ptx::cvt_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+              store_block(w, p.save0, c0 + cb * 32);
+            }
+            if (p.save1) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = ptx::cvt_bf16x2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+              store_block(w, p.save1, c0 + cb * 32);
+            }
+            act::apply<32>(p.act, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[j] = ptx::cvt_bf16x2(__uint_as_float(v[2 * j]) * __uint_as_float(u[2 * j]),
+                                     __uint_as_float(v[2 * j + 1]) * __uint_as_float(u[2 * j + 1]));
+          } else if constexpr (EPI == kEpiAct) {
+            const int row = rbase + lane, col = c0 + cb * 32;
+            if (p.bias) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (col + 8 * j < ncols) act::add8(&v[8 * j], __ldg(reinterpret_cast<const uint4*>(p.bias + col) + j));
+              }
+            }
+            if (p.save0) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = ptx::cvt_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+              store_block(w, p.save0, col);
+            }
+            act::apply<32>(p.act, v);
+            // (the residual may be Y's own buffer: a row's values are in registers before
+            // store_block's barrier lets any lane write them)
+            if (p.residual && row < pt.row_end) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (col + 8 * j < ncols)
+                  act::add8(&v[8 * j], *(reinterpret_cast<const uint4*>(p.residual + size_t(row) * ncols + col) + j));
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = ptx::cvt_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = ptx::cvt_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          }
+          store_block(w, p.out, c0 + cb * 32);
         }
       }
       ptx::tc_fence_before();
@@ -491,27 +605,35 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
     auto set_tile = [&](Cursor& c) {
       if (c.t < num_tiles) {
         const PairTile pt = pair_tile_at<DX>(grp_view, c.t, p.num_n, p.tail_split);
-        c.h0 = pt.nt * BN + int(rank) * HN;
+        c.h0 = pt.nt * TN + (TN == BN ? int(rank) * HN : 0);
         c.e = pt.e;
       }
     };
     auto advance2 = [&](Cursor& c) {
       c.ks += 2;
-      if (c.ks > nk) {
-        c.ks -= nk + 1;
+      if (c.ks >= nt) {
+        c.ks -= nt;
         c.t += npairs;
         ++c.lt;
         set_tile(c);
       }
     };
+    // Step ks of a tile belongs to the up weight: dX, past the gate's rows; forward, in rank 1.
+    auto is_up = [&](int ks) { return GATED && (DX ? ks >= nk1 : rank != 0); };
     auto scale_for = [&](const Cursor& c) {
       ItemScale sc{0u};
       if (c.t < num_tiles && c.ks < nk) {
-        const int n = DX ? c.ks * BK + geo.row : c.h0 + geo.row;
-        const int kcol = DX ? c.h0 + geo.chunk * 64 : c.ks * BK;
+        const int kr = DUAL && c.ks >= nk1 ? c.ks - nk1 : c.ks;
+        const int n = DX ? kr * BK + geo.row : c.h0 + geo.row;
+        const int kcol = DX ? c.h0 + geo.chunk * 64 : kr * BK;
         if (n < p.N && kcol < p.K) {
-          if constexpr (FMT == kFmtNF4DQ) sc = load_item_scale_dq(p.scales, p.scales2, c.e, p.N, n, kcol, p.K);
-          else sc = load_item_scale<FMT>(p.scales, n, kcol, p.K, size_t(c.e) * p.N);
+          const void* scales = p.scales;
+          const float* scales2 = p.scales2;
+          if constexpr (GATED) {
+            if (is_up(c.ks)) { scales = p.scales_up; scales2 = p.scales2_up; }
+          }
+          if constexpr (FMT == kFmtNF4DQ) sc = load_item_scale_dq(scales, scales2, c.e, p.N, n, kcol, p.K);
+          else sc = load_item_scale<FMT>(scales, n, kcol, p.K, size_t(c.e) * p.N);
         }
       }
       return sc;
@@ -525,12 +647,13 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
     while (cur.t < num_tiles) {
       const ItemScale s_pref = scale_for(pf);   // two own steps ahead
       advance2(pf);
-      const uint32_t i = uint32_t(cur.lt * (nk + 1) + cur.ks);     // pipeline step
+      const uint32_t i = uint32_t(cur.lt * nt + cur.ks);           // pipeline step
       const uint32_t sw = i % NS, pw = (i / NS) & 1u;
       const uint32_t rb = geo.op_row_base(ptx::smem_u32(wsm + sw * W_BYTES));
       if (cur.ks < nk) {
-        const int n = DX ? cur.ks * BK + geo.row : cur.h0 + geo.row;
-        const int kcol = DX ? cur.h0 + geo.chunk * 64 : cur.ks * BK;
+        const int kr = DUAL && cur.ks >= nk1 ? cur.ks - nk1 : cur.ks;
+        const int n = DX ? kr * BK + geo.row : cur.h0 + geo.row;
+        const int kcol = DX ? cur.h0 + geo.chunk * 64 : kr * BK;
         const bool valid = n < p.N && kcol < p.K;
         const uint32_t j = uint32_t(cur.lt * nk + cur.ks);          // code step
         const uint32_t scs = j % NC;
@@ -552,7 +675,30 @@ qlora_fused_gemm_kernel(const __grid_constant__ FusedParams p) {
         // LoRA step: rows of B (forward, K-major) or of A (dX, MN-major), zero padded.
         uint4 v[8];
         const __nv_bfloat16* up = p.lora_up + size_t(cur.e) * size_t(p.r) * (DX ? p.K : p.N);
-        if (!DX) {
+        if constexpr (GATED) {
+          // columns (forward) or rows (dX) j of the concatenated rank: j < r the gate's, else the
+          // up projection's; the forward's rank-0 half holds only the gate's, rank 1 the up's
+          const int jb = (cur.ks - nk) * BK;
+          if (!DX) {
+            const int n = cur.h0 + geo.row;
+            const __nv_bfloat16* src = rank != 0 ? p.lora_up_up : p.lora_up;
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) {
+              const int j = jb + jj * 8 - (rank != 0 ? p.r : 0);
+              v[jj] = (n < p.N && j >= 0 && j < p.r)
+                          ? __ldg(reinterpret_cast<const uint4*>(src + size_t(n) * p.r + j))
+                          : make_uint4(0, 0, 0, 0);
+            }
+          } else {
+            const int j = jb + geo.row, kc = cur.h0 + geo.chunk * 64;
+            const __nv_bfloat16* src = j < p.r ? up + size_t(j) * p.K
+                                               : p.lora_up_up + size_t(j - p.r) * p.K;
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj)
+              v[jj] = (j < 2 * p.r && kc < p.K) ? __ldg(reinterpret_cast<const uint4*>(src + kc + jj * 8))
+                                                : make_uint4(0, 0, 0, 0);
+          }
+        } else if (!DX) {
           const int n = cur.h0 + geo.row;
 #pragma unroll
           for (int jj = 0; jj < 8; ++jj)

@@ -132,12 +132,13 @@ struct DownParams {
   CUtensorMap tm_r;    // T: A [E, r, K] box {64, rpad, 1} SW128; U: B [E, N, r] box {rpad, 64, 1}
   const float* tensor_scale;   // NVFP4: [E], else nullptr
   __nv_bfloat16* z;    // [M, r]
-  __nv_bfloat16* zs;   // [M, r]
+  __nv_bfloat16* zs;   // [M, ldzs]
   const int32_t* offsets;      // grouped: device [E+1]; nullptr: one expert
   int* status;
   float* cpart;        // C > 1: the clusters' sums [tiles][C][128][rpad] fp32
   unsigned* ccount;    // C > 1: arrival counters [tiles][S], zero between launches
   int M, r, rpad, num_k, S, C, steps_per_split, E;
+  int ldzs;            // row pitch of zs (r, or 2r where two adapters' Zs lie side by side)
   float s;
   float zs_mul;        // an exact power of two folded into Zs (2^-8 when the next kernel decodes
                        // NVFP4 elements times 2^-8), else 1
@@ -215,7 +216,7 @@ qlora_lora_down_kernel(const __grid_constant__ DownParams p) {
     zs.z = ptx::cvt_bf16x2(v[4] * zscale, v[5] * zscale);
     zs.w = ptx::cvt_bf16x2(v[6] * zscale, v[7] * zscale);
     *reinterpret_cast<uint4*>(p.z + size_t(rw) * p.r + c) = z;
-    *reinterpret_cast<uint4*>(p.zs + size_t(rw) * p.r + c) = zs;
+    *reinterpret_cast<uint4*>(p.zs + size_t(rw) * p.ldzs + c) = zs;
   };
 
   if (warp == 0) {
@@ -351,6 +352,7 @@ struct WgradParams {
   int* status;
   int M, P0, P1, r, rpad, S, tiles0, tiles1, E;
   float s;
+  const float *l0_mul, *l0_div;  // not null: L of problem 0 holds dY * l0_mul / l0_div, taken out here
 };
 
 __global__ void __launch_bounds__(lora::kThreads, 1)
@@ -410,20 +412,21 @@ qlora_lora_wgrad_kernel(const __grid_constant__ WgradParams p) {
   const uint32_t r_bytes = 64u * rowb;
   __nv_bfloat16* out0 = p.out0 + size_t(e) * p.P0 * p.r;
   __nv_bfloat16* out1 = p.out1 + size_t(e) * p.r * p.P1;
+  const float s_out = prob == 0 && p.l0_mul ? p.s * (__ldg(p.l0_div) / __ldg(p.l0_mul)) : p.s;
   // s * the reduction for columns c .. c+7 of output row pr (dB row-major, dA transposed)
   auto write8 = [&](int pr, int c, const float (&v)[8]) {
     if (c >= p.r) return;
     if (!ptx::dcheck(pr >= 0 && pr < (prob == 0 ? p.P0 : p.P1) && e < p.E, p.status)) return;
     if (prob == 0) {
       uint4 o;
-      o.x = ptx::cvt_bf16x2(v[0] * p.s, v[1] * p.s);
-      o.y = ptx::cvt_bf16x2(v[2] * p.s, v[3] * p.s);
-      o.z = ptx::cvt_bf16x2(v[4] * p.s, v[5] * p.s);
-      o.w = ptx::cvt_bf16x2(v[6] * p.s, v[7] * p.s);
+      o.x = ptx::cvt_bf16x2(v[0] * s_out, v[1] * s_out);
+      o.y = ptx::cvt_bf16x2(v[2] * s_out, v[3] * s_out);
+      o.z = ptx::cvt_bf16x2(v[4] * s_out, v[5] * s_out);
+      o.w = ptx::cvt_bf16x2(v[6] * s_out, v[7] * s_out);
       *reinterpret_cast<uint4*>(out0 + size_t(pr) * p.r + c) = o;
     } else {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) out1[size_t(c + u) * p.P1 + pr] = __float2bfloat16_rn(v[u] * p.s);
+      for (int u = 0; u < 8; ++u) out1[size_t(c + u) * p.P1 + pr] = __float2bfloat16_rn(v[u] * s_out);
     }
   };
 

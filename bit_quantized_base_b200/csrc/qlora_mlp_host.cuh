@@ -1,0 +1,362 @@
+// qlora_mlp_host.cuh -- host side of the gated MLP and of the linear layer with bias, activation and
+// residual: argument checks, launches and entry points (included by qlora.cu).
+#pragma once
+
+namespace qlora {
+namespace {
+
+bool act_valid(int act) { return act >= QLORA_ACT_NONE && act <= QLORA_ACT_GELU_TANH; }
+
+template <int FMT, bool DX, int EPI>
+qlora_status_t launch_fused_ex_t(const FusedExParams& p, int grid, cudaStream_t st) {
+  const size_t smem = fused::smem_bytes(1);
+  if (!set_smem(qlora_fused_gemm_kernel<FMT, DX, EPI>, smem)) return QLORA_ERR_CUDA;
+  LaunchScope scope(EPI == kEpiAct ? kKindActFwd : (DX ? kKindGatedDx : kKindGatedFwd), st);
+  if (launch_pdl(qlora_fused_gemm_kernel<FMT, DX, EPI>, dim3(grid), dim3(fused::kThreads), smem, st, p) !=
+      cudaSuccess)
+    return QLORA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+template <bool DX, int EPI>
+qlora_status_t launch_fused_ex(int fmt, const FusedExParams& p, int grid, cudaStream_t st) {
+  switch (fmt) {
+    case QLORA_FMT_NF4: return launch_fused_ex_t<kFmtNF4, DX, EPI>(p, grid, st);
+    case QLORA_FMT_MXFP4: return launch_fused_ex_t<kFmtMXFP4, DX, EPI>(p, grid, st);
+    case QLORA_FMT_NVFP4: return launch_fused_ex_t<kFmtNVFP4, DX, EPI>(p, grid, st);
+    default: return launch_fused_ex_t<kFmtNF4DQ, DX, EPI>(p, grid, st);
+  }
+}
+
+bool tmap_codes(CUtensorMap* m, const qlora_weight_t* W, bool dx) {
+  const uint64_t kb = uint64_t(W->K / 2);
+  return dx ? tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, W->codes, kb, uint64_t(W->N), kb, 64, 64,
+                      CU_TENSOR_MAP_SWIZZLE_64B)
+            : tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, W->codes, kb, uint64_t(W->N), kb, 32, 128,
+                      CU_TENSOR_MAP_SWIZZLE_32B);
+}
+
+// The members of FusedParams that every variant of one layer shares: `act` and the weight Wg, Zs
+// [M, zr], `out`, and a grid of pair tiles of `tile_cols` output columns.
+qlora_status_t fill_fused(FusedExParams& p, const qlora_weight_t* W, bool dx, const void* act,
+                          const void* zs, int zr, const void* lora_up, void* out, int64_t M, int r,
+                          int tile_cols, int* status, int& grid) {
+  const int64_t Kc = dx ? W->N : W->K;
+  if (!tmap_2d(&p.tm_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, uint64_t(Kc), uint64_t(M),
+               uint64_t(Kc) * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tmap_codes(&p.tm_codes, W, dx) ||
+      !tmap_2d(&p.tm_zs, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, zs, uint64_t(zr), uint64_t(M),
+               uint64_t(zr) * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    return QLORA_ERR_CUDA;
+  p.scales = W->scales;
+  p.scales2 = W->fmt == QLORA_FMT_NF4_DQ ? W->scales2 : nullptr;
+  p.tensor_scale = W->fmt == QLORA_FMT_NVFP4 ? W->tensor_scale : nullptr;
+  p.lora_up = static_cast<const __nv_bfloat16*>(lora_up);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.status = status;
+  p.ticket = reinterpret_cast<unsigned*>(status + 1);
+  p.M = int(M);
+  p.N = int(W->N);
+  p.K = int(W->K);
+  p.r = r;
+  p.E = 1;
+  p.num_n = int(((dx ? W->K : W->N) + tile_cols - 1) / tile_cols);
+  p.num_k = int((Kc + fused::BK - 1) / fused::BK);
+  // as launch_fused: one CTA pair per two SMs, a short last wave in half tiles
+  int64_t tiles = (M + fused::BM - 1) / fused::BM * p.num_n;
+  const int64_t most = num_sms() / 2;
+  int64_t pairs = tiles < most ? tiles : most;
+  const int64_t rem = tiles % pairs;
+  if (rem > 0 && 2 * rem <= pairs && tiles > pairs) p.tail_split = int(rem);
+  tiles += p.tail_split;
+  pairs = tiles < most ? tiles : most;
+  grid = int(2 * pairs);
+  return QLORA_OK;
+}
+
+template <int NB>
+qlora_status_t launch_act_down_t(const ActDownParams& p, unsigned grid, unsigned cluster, cudaStream_t st) {
+  const size_t smem = actdown::smem_bytes(NB);
+  if (!set_smem(qlora_act_down_kernel<NB>, smem)) return QLORA_ERR_CUDA;
+  LaunchScope scope(kKindActDown, st);
+  if (launch_pdl_cluster(qlora_act_down_kernel<NB>, dim3(grid), dim3(actdown::kThreads), smem, st, p,
+                         cluster) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+// Gradients of the pre-activations and their projections (nb = 1 or 2 streams).
+qlora_status_t launch_act_down(int nb, int act, const void* dy, const void* a0, const void* a1,
+                               const void* const* B, const float* const* ts, void* const* grad,
+                               void* const* z, void* zs, float* bias_part, int64_t M, int64_t N, int r,
+                               float s, float zs_mul, void* sums, void* ws, cudaStream_t st) {
+  ActDownParams p{};
+  const int rpad = rank_pad(r);
+  const DownPlan dp = down_plan(M, N, 1, num_sms(), kDownWideCtas);
+  for (int b = 0; b < nb; ++b) {
+    if (!tmap_3d(&p.tm_r[b], B[b], uint64_t(r), uint64_t(N), 1, uint32_t(rpad), 64,
+                 swizzle_for_bytes(uint32_t(rpad) * 2)))
+      return QLORA_ERR_CUDA;
+    p.grad[b] = static_cast<__nv_bfloat16*>(grad[b]);
+    p.z[b] = static_cast<__nv_bfloat16*>(z[b]);
+  }
+  p.dy = static_cast<const __nv_bfloat16*>(dy);
+  p.a0 = static_cast<const __nv_bfloat16*>(a0);
+  p.a1 = static_cast<const __nv_bfloat16*>(a1);
+  p.zs = static_cast<__nv_bfloat16*>(zs);
+  p.ts0 = ts[0];
+  p.ts1 = nb == 2 ? ts[1] : nullptr;
+  p.bias_part = bias_part;
+  p.status = ws_status(ws);
+  if (dp.C > 1) {
+    p.cpart = static_cast<float*>(sums);
+    p.ccount = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + kDownCountOffset);
+  }
+  p.M = int(M);
+  p.N = int(N);
+  p.r = r;
+  p.rpad = rpad;
+  p.ldzs = nb * r;
+  p.num_k = dp.num_k;
+  p.S = dp.S;
+  p.C = dp.C;
+  p.sps = dp.sps;
+  p.act = act;
+  p.s = s;
+  p.zs_mul = zs_mul;
+  const unsigned grid = unsigned(dp.tiles * dp.S * dp.C);
+  return nb == 2 ? launch_act_down_t<2>(p, grid, unsigned(dp.S), st)
+                 : launch_act_down_t<1>(p, grid, unsigned(dp.S), st);
+}
+
+// Runs `side_work` on the device's side stream beside `main_work` on `s`, joined into `s` again.
+template <class F, class G>
+qlora_status_t fork_join(cudaStream_t s, F&& side_work, G&& main_work) {
+  SideStream* side = side_stream();
+  if (!side) {
+    const qlora_status_t st = main_work();
+    return st != QLORA_OK ? st : side_work(s);
+  }
+  const int slot = side->next.fetch_add(1, std::memory_order_relaxed) % SideStream::kEvents;
+  if (cudaEventRecord(side->fork[slot], s) != cudaSuccess ||
+      cudaStreamWaitEvent(side->stream, side->fork[slot], 0) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  qlora_status_t st = side_work(side->stream);
+  if (cudaEventRecord(side->join[slot], side->stream) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (st == QLORA_OK) st = main_work();
+  if (cudaStreamWaitEvent(s, side->join[slot], 0) != cudaSuccess) return QLORA_ERR_CUDA;
+  return st;
+}
+
+qlora_status_t check_gated(const qlora_weight_t* Wg, const qlora_weight_t* Wu, int act, int64_t M, int r) {
+  qlora_status_t st = check_common(Wg, M, r);
+  if (st != QLORA_OK) return st;
+  if ((st = check_weight(Wu)) != QLORA_OK) return st;
+  if (Wg->N != Wu->N || Wg->K != Wu->K || !act_valid(act)) return QLORA_ERR_INVALID_ARG;
+  return Wg->fmt == Wu->fmt ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
+}
+
+const float* ts_of(const qlora_weight_t* W) {
+  return W->fmt == QLORA_FMT_NVFP4 ? W->tensor_scale : nullptr;
+}
+
+}  // namespace
+}  // namespace qlora
+
+extern "C" {
+
+qlora_status_t qlora_gated_mlp_fwd(const qlora_weight_t* Wg, const qlora_weight_t* Wu, int act,
+                                   const void* X, const void* Ag, const void* Bg, const void* Au,
+                                   const void* Bu, void* H, void* G, void* U, void* T_save, int64_t M,
+                                   int r, float scale, void* ws, size_t ws_bytes,
+                                   qlora_stream_t stream) {
+  qlora_status_t st = check_gated(Wg, Wu, act, M, r);
+  if (st != QLORA_OK) return st;
+  if (!act_ok(X, M) || !ptr_ok(Ag) || !ptr_ok(Bg) || !ptr_ok(Au) || !ptr_ok(Bu) || !act_ok(H, M) ||
+      !opt_ok(G) || !opt_ok(U) || !opt_ok(T_save))
+    return QLORA_ERR_INVALID_ARG;
+  const MlpLayout L = mlp_layout(Wg->N, Wg->K, M, r, 2, false, num_sms());
+  if (!ws || !aligned16(ws) || ws_bytes < L.partial) return QLORA_ERR_WORKSPACE;
+  if (M == 0) return QLORA_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  uint8_t* T = T_save ? static_cast<uint8_t*>(T_save) : w + L.t;
+  const size_t mr = size_t(M) * size_t(r) * 2;
+  for (int i = 0; i < 2; ++i) {
+    st = launch_lora_down(false, X, M, Wg->K, i ? Au : Ag, r, scale, ts_of(i ? Wu : Wg), T + i * mr,
+                          w + L.zs + size_t(i) * r * 2, ws_status(ws), nullptr, 1, false,
+                          kDownCtasBesidePair, s, 1.0f, 0, nullptr, nullptr, 2 * r);
+    if (st != QLORA_OK) return st;
+  }
+  FusedExParams p{};
+  int grid = 0;
+  st = fill_fused(p, Wg, false, X, w + L.zs, 2 * r, Bg, H, M, r, fused::HN, ws_status(ws), grid);
+  if (st != QLORA_OK) return st;
+  if (!tmap_codes(&p.tm_codes_up, Wu, false)) return QLORA_ERR_CUDA;
+  p.scales_up = Wu->scales;
+  p.scales2_up = Wu->scales2;
+  p.tensor_scale_up = ts_of(Wu);
+  p.lora_up_up = static_cast<const __nv_bfloat16*>(Bu);
+  p.save0 = static_cast<__nv_bfloat16*>(G);
+  p.save1 = static_cast<__nv_bfloat16*>(U);
+  p.act = act;
+  return launch_fused_ex<false, kEpiGated>(Wg->fmt, p, grid, s);
+}
+
+qlora_status_t qlora_gated_mlp_bwd(const qlora_weight_t* Wg, const qlora_weight_t* Wu, int act,
+                                   const void* X, const void* Ag, const void* Bg, const void* Au,
+                                   const void* Bu, const void* T, const void* G, const void* U,
+                                   const void* dH, void* dX, void* dAg, void* dBg, void* dAu, void* dBu,
+                                   int64_t M, int r, float scale, void* ws, size_t ws_bytes,
+                                   qlora_stream_t stream) {
+  qlora_status_t st = check_gated(Wg, Wu, act, M, r);
+  if (st != QLORA_OK) return st;
+  if (!act_ok(X, M) || !ptr_ok(Ag) || !ptr_ok(Bg) || !ptr_ok(Au) || !ptr_ok(Bu) || !opt_ok(T) ||
+      !act_ok(G, M) || !act_ok(U, M) || !act_ok(dH, M) || !opt_ok(dX) || !ptr_ok(dAg) || !ptr_ok(dBg) ||
+      !ptr_ok(dAu) || !ptr_ok(dBu))
+    return QLORA_ERR_INVALID_ARG;
+  const int64_t N = Wg->N, K = Wg->K;
+  const MlpLayout L = mlp_layout(N, K, M, r, 2, true, num_sms());
+  if (!ws || !aligned16(ws) || ws_bytes < L.partial) return QLORA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    for (void* d : {dAg, dAu})
+      if (cudaMemsetAsync(d, 0, size_t(r) * K * 2, s) != cudaSuccess) return QLORA_ERR_CUDA;
+    for (void* d : {dBg, dBu})
+      if (cudaMemsetAsync(d, 0, size_t(N) * r * 2, s) != cudaSuccess) return QLORA_ERR_CUDA;
+    return QLORA_OK;
+  }
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const size_t mr = size_t(M) * size_t(r) * 2, mn = size_t(M) * size_t(N) * 2;
+  const uint8_t* Ts = static_cast<const uint8_t*>(T);
+  if (!T) {   // recomputed with the forward's plan: the forward's T bit for bit
+    for (int i = 0; i < 2; ++i) {
+      st = launch_lora_down(false, X, M, K, i ? Au : Ag, r, scale, ts_of(i ? Wu : Wg), w + L.t + i * mr,
+                            w + L.zs + size_t(i) * r * 2, ws_status(ws), nullptr, 1, false,
+                            kDownCtasBesidePair, s, 1.0f, 0, nullptr, nullptr, 2 * r);
+      if (st != QLORA_OK) return st;
+    }
+    Ts = w + L.t;
+  }
+  void* const grad[2] = {w + L.grad, w + L.grad + mn};
+  void* const z[2] = {w + L.u, w + L.u + mr};
+  const void* const Bs[2] = {Bg, Bu};
+  const float* const ts[2] = {ts_of(Wg), ts_of(Wu)};
+  st = launch_act_down(2, act, dH, G, U, Bs, ts, grad, z, w + L.zs, nullptr, M, N, r, scale, 1.0f,
+                       w + L.sums, ws, s);
+  if (st != QLORA_OK) return st;
+  auto wgrads = [&](cudaStream_t q) {
+    qlora_status_t e = launch_wgrad(X, grad[0], Ts, z[0], M, N, K, r, scale, dAg, dBg, ws, nullptr, 1, false, q);
+    if (e != QLORA_OK) return e;
+    return launch_wgrad(X, grad[1], Ts + mr, z[1], M, N, K, r, scale, dAu, dBu, ws, nullptr, 1, false, q,
+                        ts[1], ts[1] ? ts[0] : nullptr);
+  };
+  if (!dX) return wgrads(s);
+  return fork_join(s, wgrads, [&]() {
+    FusedExParams p{};
+    int grid = 0;
+    qlora_status_t e = fill_fused(p, Wg, true, grad[0], w + L.zs, 2 * r, Ag, dX, M, r, fused::BN,
+                                  ws_status(ws), grid);
+    if (e != QLORA_OK) return e;
+    if (!tmap_codes(&p.tm_codes_up, Wu, true) ||
+        !tmap_2d(&p.tm_act_up, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, grad[1], uint64_t(N), uint64_t(M),
+                 uint64_t(N) * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+      return QLORA_ERR_CUDA;
+    p.scales_up = Wu->scales;
+    p.scales2_up = Wu->scales2;
+    p.lora_up_up = static_cast<const __nv_bfloat16*>(Au);
+    return launch_fused_ex<true, kEpiGated>(Wg->fmt, p, grid, s);
+  });
+}
+
+qlora_status_t qlora_linear_act_fwd(const qlora_weight_t* W, const void* X, const void* A, const void* B,
+                                    const void* bias, int act, const void* residual, void* Y,
+                                    void* Z_save, void* T_save, int64_t M, int r, float scale, void* ws,
+                                    size_t ws_bytes, qlora_stream_t stream) {
+  qlora_status_t st = check_common(W, M, r);
+  if (st != QLORA_OK) return st;
+  if (!act_valid(act) || !act_ok(X, M) || !ptr_ok(A) || !ptr_ok(B) || !opt_ok(bias) || !opt_ok(residual) ||
+      !act_ok(Y, M) || !opt_ok(Z_save) || !opt_ok(T_save))
+    return QLORA_ERR_INVALID_ARG;
+  const MlpLayout L = mlp_layout(W->N, W->K, M, r, 1, false, num_sms());
+  if (!ws || !aligned16(ws) || ws_bytes < L.partial) return QLORA_ERR_WORKSPACE;
+  if (M == 0) return QLORA_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  st = launch_lora_down(false, X, M, W->K, A, r, scale, ts_of(W), T_save ? T_save : w + L.t, w + L.zs,
+                        ws_status(ws), nullptr, 1, false, kDownCtasBesidePair, s);
+  if (st != QLORA_OK) return st;
+  FusedExParams p{};
+  int grid = 0;
+  st = fill_fused(p, W, false, X, w + L.zs, r, B, Y, M, r, fused::BN, ws_status(ws), grid);
+  if (st != QLORA_OK) return st;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.save0 = static_cast<__nv_bfloat16*>(Z_save);
+  p.act = act;
+  return launch_fused_ex<false, kEpiAct>(W->fmt, p, grid, s);
+}
+
+qlora_status_t qlora_linear_act_bwd(const qlora_weight_t* W, const void* X, const void* A, const void* B,
+                                    const void* T, const void* Z, int act, const void* dY, void* dX,
+                                    void* dA, void* dB, void* dbias, int64_t M, int r, float scale,
+                                    void* ws, size_t ws_bytes, qlora_stream_t stream) {
+  qlora_status_t st = check_common(W, M, r);
+  if (st != QLORA_OK) return st;
+  if (!act_valid(act) || !opt_ok(Z) || (act != QLORA_ACT_NONE && !act_ok(Z, M)) || !opt_ok(dbias))
+    return QLORA_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (act == QLORA_ACT_NONE && !dbias)   // dZ is dY: the layer's own backward pass
+    return run_bwd(W, 1, nullptr, false, X, A, B, T, dY, dX, dA, dB, M, r, scale, ws, ws_bytes, s);
+  if (!act_ok(X, M) || !ptr_ok(A) || !ptr_ok(B) || !opt_ok(T) || !act_ok(dY, M) || !opt_ok(dX) ||
+      !ptr_ok(dA) || !ptr_ok(dB))
+    return QLORA_ERR_INVALID_ARG;
+  const int64_t N = W->N, K = W->K;
+  const MlpLayout L = mlp_layout(N, K, M, r, 1, true, num_sms());
+  if (!ws || !aligned16(ws) || ws_bytes < L.partial) return QLORA_ERR_WORKSPACE;
+  if (M == 0) {
+    if (cudaMemsetAsync(dA, 0, size_t(r) * K * 2, s) != cudaSuccess ||
+        cudaMemsetAsync(dB, 0, size_t(N) * r * 2, s) != cudaSuccess ||
+        (dbias && cudaMemsetAsync(dbias, 0, size_t(N) * 2, s) != cudaSuccess))
+      return QLORA_ERR_CUDA;
+    return QLORA_OK;
+  }
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  float* part = reinterpret_cast<float*>(w + L.partial);
+  const size_t region = ws_bytes - L.partial;
+  const bool short_dx = dX && short_fits(W, M, 1, true, region);
+  const bool stream_dx = dX && !short_dx && stream_fits(W, M, 1, true, region);
+  if (!T) {
+    st = launch_lora_down(false, X, M, K, A, r, scale, ts_of(W), w + L.t, w + L.zs, ws_status(ws), nullptr,
+                          1, false, kDownCtasBesidePair, s);
+    if (st != QLORA_OK) return st;
+    T = w + L.t;
+  }
+  void* const grad[1] = {act == QLORA_ACT_NONE ? nullptr : w + L.grad};
+  void* const z[1] = {w + L.u};
+  const void* const Bs[1] = {B};
+  const float* const ts[1] = {ts_of(W)};
+  float* bias_part = dbias ? reinterpret_cast<float*>(w + L.bias) : nullptr;
+  st = launch_act_down(1, act, dY, act == QLORA_ACT_NONE ? nullptr : Z, nullptr, Bs, ts, grad, z, w + L.zs,
+                       bias_part, M, N, r, scale, short_dx ? short_zs_mul(W) : 1.0f, w + L.sums, ws, s);
+  if (st != QLORA_OK) return st;
+  const void* dZ = act == QLORA_ACT_NONE ? dY : grad[0];
+  auto side_work = [&](cudaStream_t q) {
+    const qlora_status_t e = launch_wgrad(X, dZ, T, z[0], M, N, K, r, scale, dA, dB, ws, nullptr, 1, false, q);
+    if (e != QLORA_OK || !dbias) return e;
+    BiasSumParams b{bias_part, static_cast<__nv_bfloat16*>(dbias), int((M + 127) / 128), int(N)};
+    LaunchScope scope(kKindBiasSum, q);
+    if (launch_pdl(qlora_bias_sum_kernel, dim3(unsigned((N + 255) / 256)), dim3(256), 0, q, b) != cudaSuccess ||
+        cudaGetLastError() != cudaSuccess)
+      return QLORA_ERR_CUDA;
+    return QLORA_OK;
+  };
+  if (!dX) return side_work(s);
+  return fork_join(s, side_work, [&]() {
+    if (short_dx) return launch_short(W, true, dZ, w + L.zs, A, dX, M, r, ws, part, region, s);
+    if (stream_dx) return launch_stream(W, true, dZ, w + L.zs, A, dX, M, r, ws_status(ws), part, region, s);
+    return launch_fused(W, true, dZ, w + L.zs, A, dX, M, r, ws_status(ws), nullptr, 1, false, s);
+  });
+}
+
+}  // extern "C"

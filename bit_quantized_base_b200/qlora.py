@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_PKG, "libqlora_debug.so" if os.environ.get("QLORA_LIBRA
 FMT = {"nf4": 0, "mxfp4": 1, "nvfp4": 2, "nf4dq": 3}
 BLOCK = {"nf4": 64, "mxfp4": 32, "nvfp4": 16}
 OP_FWD, OP_BWD, OP_GROUPED_FWD, OP_GROUPED_BWD, OP_FWD_W4A8 = 0, 1, 2, 3, 4
+OP_GATED_MLP_FWD, OP_GATED_MLP_BWD, OP_ACT_FWD, OP_ACT_BWD = 5, 6, 7, 8
+ACT = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
 
 STATUS = {0: "QLORA_OK", 1: "QLORA_ERR_INVALID_ARG", 2: "QLORA_ERR_UNSUPPORTED",
           3: "QLORA_ERR_WORKSPACE", 4: "QLORA_ERR_CUDA", 5: "QLORA_ERR_DEVICE_TIMEOUT"}
@@ -33,7 +35,9 @@ EXPORTS = ("qlora_workspace_size", "qlora_workspace_init", "qlora_linear_fwd", "
            "qlora_linear_fwd_noalloc_status", "qlora_linear_fwd_w4a8", "qlora_mxfp8_quantize",
            "qlora_debug_decode_rate", "qlora_quantize", "qlora_merge_requantize",
            "qlora_loftq_workspace_size", "qlora_loftq", "qlora_linear_fwd_w4a8_codes",
-           "qlora_rmsnorm_fwd", "qlora_rmsnorm_workspace_size", "qlora_rmsnorm_bwd")
+           "qlora_rmsnorm_fwd", "qlora_rmsnorm_workspace_size", "qlora_rmsnorm_bwd",
+           "qlora_gated_mlp_fwd", "qlora_gated_mlp_bwd", "qlora_linear_act_fwd",
+           "qlora_linear_act_bwd")
 
 
 class QLoraError(RuntimeError):
@@ -86,6 +90,14 @@ def _load():
                                         c.c_size_t, P]
     L.qlora_linear_fwd_w4a8_codes.argtypes = [W, P, P, P, P, P, P, P, c.c_int64, c.c_int, c.c_float,
                                               P, c.c_size_t, P]
+    L.qlora_gated_mlp_fwd.argtypes = [W, W, c.c_int] + [P] * 9 + [c.c_int64, c.c_int, c.c_float, P,
+                                                                  c.c_size_t, P]
+    L.qlora_gated_mlp_bwd.argtypes = [W, W, c.c_int] + [P] * 14 + [c.c_int64, c.c_int, c.c_float, P,
+                                                                   c.c_size_t, P]
+    L.qlora_linear_act_fwd.argtypes = [W, P, P, P, P, c.c_int, P, P, P, P, c.c_int64, c.c_int,
+                                       c.c_float, P, c.c_size_t, P]
+    L.qlora_linear_act_bwd.argtypes = [W, P, P, P, P, P, c.c_int, P, P, P, P, P, c.c_int64, c.c_int,
+                                       c.c_float, P, c.c_size_t, P]
     L.qlora_rmsnorm_fwd.argtypes = [P, P, P, c.c_float, P, P, P, P, P, c.c_int64, c.c_int64, P]
     L.qlora_rmsnorm_workspace_size.argtypes = [c.c_int64, c.c_int64]
     L.qlora_rmsnorm_workspace_size.restype = c.c_size_t
@@ -104,7 +116,8 @@ def _load():
                  "qlora_debug_dequant", "qlora_debug_wait_timeout", "qlora_debug_decode_rate",
                  "qlora_quantize", "qlora_merge_requantize", "qlora_loftq",
                  "qlora_linear_fwd_w4a8", "qlora_mxfp8_quantize", "qlora_linear_fwd_w4a8_codes",
-                 "qlora_rmsnorm_fwd", "qlora_rmsnorm_bwd",
+                 "qlora_rmsnorm_fwd", "qlora_rmsnorm_bwd", "qlora_gated_mlp_fwd",
+                 "qlora_gated_mlp_bwd", "qlora_linear_act_fwd", "qlora_linear_act_bwd",
                  "qlora_profile_enable",
                  "qlora_profile_reset", "qlora_profile_read"):
         getattr(L, name).restype = c.c_int
@@ -252,6 +265,71 @@ def qlora_rmsnorm_bwd(S, rstd, gamma, eps, dY, dS_in, dS, dgamma, M, K, ws=None,
                                  _on(stream, dev)), "qlora_rmsnorm_bwd")
 
 
+def _act(act):
+    return ACT[act] if isinstance(act, str) else int(act)
+
+
+def qlora_gated_mlp_fwd(Wg: Weight, Wu: Weight, act, X, Ag, Bg, Au, Bu, H, G, U, T_save, M, r, scale,
+                        ws, stream=None):
+    """H = act(G) * U, G and U the gate's and up projection's LoRA layers on X; G, U [M,N] and
+    T_save [2,M,r] are saved unless None.  act: "none", "silu", "gelu" or "gelu_tanh"."""
+    N, K, bf = Wg.N, Wg.K, torch.bfloat16
+    dev, x, ag, bg, au, bu, h, g, u, t, w = _args(
+        "qlora_gated_mlp_fwd", ("X", X, bf, M * K, M > 0), ("Ag", Ag, bf, r * K, True),
+        ("Bg", Bg, bf, N * r, True), ("Au", Au, bf, r * K, True), ("Bu", Bu, bf, N * r, True),
+        ("H", H, bf, M * N, M > 0), ("G", G, bf, M * N, False), ("U", U, bf, M * N, False),
+        ("T_save", T_save, bf, 2 * M * r, False), ("ws", ws, torch.uint8, -1, False))
+    _check(lib.qlora_gated_mlp_fwd(Wg.ref, Wu.ref, _act(act), x, ag, bg, au, bu, h, g, u, t, M, r, scale, w,
+                                   0 if ws is None else ws.numel(), _on(stream, dev)), "qlora_gated_mlp_fwd")
+
+
+def qlora_gated_mlp_bwd(Wg: Weight, Wu: Weight, act, X, Ag, Bg, Au, Bu, T, G, U, dH, dX, dAg, dBg, dAu,
+                        dBu, M, r, scale, ws, stream=None):
+    """Gradients of qlora_gated_mlp_fwd from its saved G, U [M,N] and T [2,M,r] (None: recomputed);
+    dX may be None."""
+    N, K, bf = Wg.N, Wg.K, torch.bfloat16
+    dev, x, ag, bg, au, bu, t, g, u, dh, dx, dag, dbg, dau, dbu, w = _args(
+        "qlora_gated_mlp_bwd", ("X", X, bf, M * K, M > 0), ("Ag", Ag, bf, r * K, True),
+        ("Bg", Bg, bf, N * r, True), ("Au", Au, bf, r * K, True), ("Bu", Bu, bf, N * r, True),
+        ("T", T, bf, 2 * M * r, False), ("G", G, bf, M * N, M > 0), ("U", U, bf, M * N, M > 0),
+        ("dH", dH, bf, M * N, M > 0), ("dX", dX, bf, M * K, False), ("dAg", dAg, bf, r * K, True),
+        ("dBg", dBg, bf, N * r, True), ("dAu", dAu, bf, r * K, True), ("dBu", dBu, bf, N * r, True),
+        ("ws", ws, torch.uint8, -1, False))
+    _check(lib.qlora_gated_mlp_bwd(Wg.ref, Wu.ref, _act(act), x, ag, bg, au, bu, t, g, u, dh, dx, dag, dbg,
+                                   dau, dbu, M, r, scale, w, 0 if ws is None else ws.numel(),
+                                   _on(stream, dev)), "qlora_gated_mlp_bwd")
+
+
+def qlora_linear_act_fwd(W: Weight, X, A, B, bias, act, residual, Y, Z_save, T_save, M, r, scale, ws,
+                         stream=None):
+    """Y = act(Z) + residual, Z = the LoRA layer on X + bias; bias [N], residual [M,N], Z_save [M,N]
+    and T_save [M,r] may be None."""
+    N, K, bf = W.N, W.K, torch.bfloat16
+    dev, x, a, b, bi, re, y, z, t, w = _args(
+        "qlora_linear_act_fwd", ("X", X, bf, M * K, M > 0), ("A", A, bf, r * K, True),
+        ("B", B, bf, N * r, True), ("bias", bias, bf, N, False), ("residual", residual, bf, M * N, False),
+        ("Y", Y, bf, M * N, M > 0), ("Z_save", Z_save, bf, M * N, False),
+        ("T_save", T_save, bf, M * r, False), ("ws", ws, torch.uint8, -1, False))
+    _check(lib.qlora_linear_act_fwd(W.ref, x, a, b, bi, _act(act), re, y, z, t, M, r, scale, w,
+                                    0 if ws is None else ws.numel(), _on(stream, dev)),
+           "qlora_linear_act_fwd")
+
+
+def qlora_linear_act_bwd(W: Weight, X, A, B, T, Z, act, dY, dX, dA, dB, dbias, M, r, scale, ws,
+                         stream=None):
+    """Gradients of qlora_linear_act_fwd from its saved Z [M,N] (None for act "none") and T [M,r]
+    (None: recomputed); dX and dbias may be None."""
+    N, K, bf = W.N, W.K, torch.bfloat16
+    dev, x, a, b, t, z, dy, dx, da, db, di, w = _args(
+        "qlora_linear_act_bwd", ("X", X, bf, M * K, M > 0), ("A", A, bf, r * K, True),
+        ("B", B, bf, N * r, True), ("T", T, bf, M * r, False), ("Z", Z, bf, M * N, False),
+        ("dY", dY, bf, M * N, M > 0), ("dX", dX, bf, M * K, False), ("dA", dA, bf, r * K, True),
+        ("dB", dB, bf, N * r, True), ("dbias", dbias, bf, N, False), ("ws", ws, torch.uint8, -1, False))
+    _check(lib.qlora_linear_act_bwd(W.ref, x, a, b, t, z, _act(act), dy, dx, da, db, di, M, r, scale, w,
+                                    0 if ws is None else ws.numel(), _on(stream, dev)),
+           "qlora_linear_act_bwd")
+
+
 def qlora_mxfp8_quantize(X, M, K, codes, scales, stream=None):
     """X [M,K] bf16 -> codes [M,K] uint8 (E4M3) and scales [M,K/32] uint8 (E8M0)."""
     _check(lib.qlora_mxfp8_quantize(_p(X), int(M), int(K), _p(codes), _p(scales), _stream(stream)),
@@ -382,7 +460,7 @@ def qlora_profile_reset():
 def qlora_profile_read():
     """{kind: (launches, total_ms)} of the launches recorded since the last reset."""
     n = ctypes.c_int(0)
-    cap = 16
+    cap = 32
     names = (ctypes.c_char_p * cap)()
     counts = (ctypes.c_int * cap)()
     ms = (ctypes.c_double * cap)()

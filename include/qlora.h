@@ -119,8 +119,20 @@ typedef enum {
   QLORA_OP_BWD = 1,
   QLORA_OP_GROUPED_FWD = 2,
   QLORA_OP_GROUPED_BWD = 3,
-  QLORA_OP_FWD_W4A8 = 4       /* qlora_linear_fwd_w4a8 */
+  QLORA_OP_FWD_W4A8 = 4,      /* qlora_linear_fwd_w4a8 */
+  QLORA_OP_GATED_MLP_FWD = 5, /* qlora_gated_mlp_fwd (W: either of its weights) */
+  QLORA_OP_GATED_MLP_BWD = 6, /* qlora_gated_mlp_bwd; its workspace also serves the forward */
+  QLORA_OP_ACT_FWD = 7,       /* qlora_linear_act_fwd */
+  QLORA_OP_ACT_BWD = 8        /* qlora_linear_act_bwd; its workspace also serves the forward */
 } qlora_op_t;
+
+/* Activations of the gated MLP and of the linear layer with an epilogue, taken of the fp32 value. */
+typedef enum {
+  QLORA_ACT_NONE = 0,
+  QLORA_ACT_SILU = 1,      /* z / (1 + e^-z) */
+  QLORA_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
+  QLORA_ACT_GELU_TANH = 3  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+} qlora_act_t;
 
 /* Bytes of device workspace `op` needs for these shapes (E = number of experts for the grouped
  * ops, ignored otherwise; for the grouped ops M is the total row count).  Returns 0 for invalid
@@ -284,6 +296,71 @@ QLORA_API qlora_status_t qlora_rmsnorm_bwd(const void* S, const float* rstd, con
                                            void* dgamma, int64_t M, int64_t K, void* ws,
                                            size_t ws_bytes, qlora_stream_t stream);
 
+/* Gated MLP block on two frozen 4-bit weights with their adapters (the gate and up projections of a
+ * decoder layer), both products, the activation and the product of the two in one kernel:
+ *   G = X deq(Wg)^T + s (X Ag^T) Bg^T     U = X deq(Wu)^T + s (X Au^T) Bu^T     H = act(G) U
+ * act and the product are taken of the fp32 accumulators; H, and G and U where they are saved, are
+ * each rounded once.
+ *   Wg, Wu: the same format, N and K (different formats: QLORA_ERR_UNSUPPORTED);
+ *   X [M,K]; Ag, Au [r,K]; Bg, Bu [N,r]; act: qlora_act_t;
+ *   H [M,N] out; G, U [M,N] out or NULL (what qlora_gated_mlp_bwd reads; either alone may be NULL);
+ *   T_save [2,M,r] out or NULL: X Ag^T, then X Au^T;
+ *   ws >= qlora_workspace_size(QLORA_OP_GATED_MLP_FWD, Wg, M, r, 0), initialised as for every call.
+ * Limits, errors and conventions as qlora_linear_fwd; M = 0 is a no-op.  H, G and U must not overlap
+ * X or each other. */
+QLORA_API qlora_status_t qlora_gated_mlp_fwd(const qlora_weight_t* Wg, const qlora_weight_t* Wu,
+                                             int act, const void* X, const void* Ag, const void* Bg,
+                                             const void* Au, const void* Bu, void* H, void* G,
+                                             void* U, void* T_save, int64_t M, int r, float scale,
+                                             void* ws, size_t ws_bytes, qlora_stream_t stream);
+
+/* Backward of qlora_gated_mlp_fwd.  With dG = dH U act'(G) and dU = dH act(G) (formed in fp32 from the
+ * saved bf16 G and U):
+ *   dX = dG deq(Wg) + dU deq(Wu) + s (dG Bg) Ag + s (dU Bu) Au
+ *   dAg = s (dG Bg)^T X    dBg = s dG^T Tg    dAu = s (dU Bu)^T X    dBu = s dU^T Tu
+ * dG and dU are rounded to bf16 as operands of the products with the weights and T; the rank-r
+ * products dG Bg and dU Bu take them unrounded.
+ *   T [2,M,r]: the forward's T_save, or NULL to recompute it from X, Ag and Au;
+ *   G, U [M,N]: the forward's; dH [M,N]; dX [M,K] out or NULL; dAg, dAu [r,K], dBg, dBu [N,r] out;
+ *   ws >= qlora_workspace_size(QLORA_OP_GATED_MLP_BWD, ...): holds dG and dU, 4 M N bytes.
+ * NVFP4: the up gradient enters the shared accumulator times ts_up / ts_gate, so the two tensor
+ * scales must lie within a factor of 2^60 of each other.  M = 0 overwrites the adapter gradients
+ * with zeros.  Deterministic. */
+QLORA_API qlora_status_t qlora_gated_mlp_bwd(const qlora_weight_t* Wg, const qlora_weight_t* Wu,
+                                             int act, const void* X, const void* Ag, const void* Bg,
+                                             const void* Au, const void* Bu, const void* T,
+                                             const void* G, const void* U, const void* dH, void* dX,
+                                             void* dAg, void* dBg, void* dAu, void* dBu, int64_t M,
+                                             int r, float scale, void* ws, size_t ws_bytes,
+                                             qlora_stream_t stream);
+
+/* qlora_linear_fwd with bias, activation and residual in its epilogue:
+ *   Z = X deq(W)^T + s (X A^T) B^T + bias        Y = act(Z) + residual
+ * all of it on the fp32 accumulator, rounded once (a down projection added to the residual stream:
+ * act NONE and a residual; a biased or activated projection: the others).
+ *   bias [N] bf16 or NULL; residual [M,N] bf16 or NULL, may be the same buffer as Y;
+ *   Z_save [M,N] out or NULL: Z rounded to bf16, what qlora_linear_act_bwd reads (act NONE needs
+ *   none); T_save [M,r] out or NULL; ws >= qlora_workspace_size(QLORA_OP_ACT_FWD, W, M, r, 0).
+ * Limits, errors and conventions as qlora_linear_fwd. */
+QLORA_API qlora_status_t qlora_linear_act_fwd(const qlora_weight_t* W, const void* X, const void* A,
+                                              const void* B, const void* bias, int act,
+                                              const void* residual, void* Y, void* Z_save,
+                                              void* T_save, int64_t M, int r, float scale, void* ws,
+                                              size_t ws_bytes, qlora_stream_t stream);
+
+/* Backward of qlora_linear_act_fwd.  With dZ = dY act'(Z):
+ *   dX = dZ deq(W) + s (dZ B) A    dA = s (dZ B)^T X    dB = s dZ^T T    dbias[n] = sum_m dZ[m,n]
+ * (the residual's gradient is dY itself).  dbias and dZ B take dZ unrounded.
+ *   T [M,r] or NULL (recomputed); Z [M,N]: the forward's Z_save, may be NULL for act NONE;
+ *   dX [M,K] out or NULL; dA [r,K], dB [N,r] out; dbias [N] bf16 out or NULL;
+ *   ws >= qlora_workspace_size(QLORA_OP_ACT_BWD, W, M, r, 0).
+ * act NONE without dbias is qlora_linear_bwd.  M = 0 overwrites the parameter gradients with zeros. */
+QLORA_API qlora_status_t qlora_linear_act_bwd(const qlora_weight_t* W, const void* X, const void* A,
+                                              const void* B, const void* T, const void* Z, int act,
+                                              const void* dY, void* dX, void* dA, void* dB,
+                                              void* dbias, int64_t M, int r, float scale, void* ws,
+                                              size_t ws_bytes, qlora_stream_t stream);
+
 /* Synchronise `stream` and read the status word of qlora_linear_fwd_noalloc's fixed scratch on
  * the current device: QLORA_OK, or the device-side error of the last no-alloc call (each call
  * clears it when it starts).  Allocates nothing.  Not for the compute path. */
@@ -388,7 +465,8 @@ QLORA_API qlora_status_t qlora_debug_decode_rate(int fmt, int iters,
  * returns, per kernel kind, the launch count and total milliseconds.  Kinds: "fused_fwd",
  * "fused_dx", "lora_down_T", "lora_down_U", "lora_wgrad" (grouped variants add "grouped_"),
  * "stream_fwd", "stream_dx", "stream_reduce" (batches of 65-256 rows), "short_fwd", "short_dx"
- * (batches of up to 64 rows), "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma".
+ * (batches of up to 64 rows), "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma",
+ * "gated_fwd", "gated_dx", "act_fwd", "act_down" (gradients behind an activation), "bias_sum".
  * Host-side bookkeeping only; the compute path is unchanged when profiling is off. */
 QLORA_API int64_t qlora_launch_count(void);
 QLORA_API qlora_status_t qlora_profile_enable(int enable);
