@@ -18,6 +18,7 @@
 #include "qlora_w4a8.cuh"
 #include "qlora_norm.cuh"
 #include "qlora_act_down.cuh"
+#include "qlora_narrow.cuh"
 #include <algorithm>
 #include <utility>
 #include "qlora_quant.cuh"
@@ -389,14 +390,15 @@ enum Kind : int {
   kKindGFusedFwd, kKindGFusedDx, kKindGDownT, kKindGDownU, kKindGWgrad,
   kKindStreamFwd, kKindStreamDx, kKindStreamReduce, kKindShortFwd, kKindShortDx,
   kKindW4a8Quant, kKindW4a8Gemm, kKindNormFwd, kKindNormBwd, kKindNormDgamma,
-  kKindGatedFwd, kKindGatedDx, kKindActFwd, kKindActDown, kKindBiasSum, kNumKinds
+  kKindGatedFwd, kKindGatedDx, kKindActFwd, kKindActDown, kKindBiasSum,
+  kKindNarrowDown, kNumKinds
 };
 const char* const kKindNames[kNumKinds] = {
     "fused_fwd", "fused_dx", "lora_down_T", "lora_down_U", "lora_wgrad",
     "grouped_fused_fwd", "grouped_fused_dx", "grouped_lora_down_T", "grouped_lora_down_U",
     "grouped_lora_wgrad", "stream_fwd", "stream_dx", "stream_reduce", "short_fwd", "short_dx",
     "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma",
-    "gated_fwd", "gated_dx", "act_fwd", "act_down", "bias_sum"};
+    "gated_fwd", "gated_dx", "act_fwd", "act_down", "bias_sum", "narrow_down_T"};
 constexpr int kMaxProfiled = 65536;
 
 std::atomic<int64_t> g_launches{0};

@@ -5,6 +5,10 @@
 namespace qlora {
 namespace {
 
+const float* ts_of(const qlora_weight_t* W) {
+  return W->fmt == QLORA_FMT_NVFP4 ? W->tensor_scale : nullptr;
+}
+
 bool act_valid(int act) { return act >= QLORA_ACT_NONE && act <= QLORA_ACT_GELU_TANH; }
 
 template <int FMT, bool DX, int EPI>
@@ -148,6 +152,151 @@ qlora_status_t fork_join(cudaStream_t s, F&& side_work, G&& main_work) {
   return st;
 }
 
+// ------------------------------------------------------------------------- batches of up to 64 rows
+template <int NB>
+qlora_status_t launch_narrow_down_t(const NarrowDownParams& p, unsigned groups, cudaStream_t st) {
+  if (!set_smem(qlora_narrow_down_kernel<NB>, 0)) return QLORA_ERR_CUDA;
+  LaunchScope scope(kKindNarrowDown, st);
+  if (launch_pdl_cluster(qlora_narrow_down_kernel<NB>, dim3(groups * unsigned(p.S)), dim3(narrow::kThreads), 0,
+                         st, p, unsigned(p.S)) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+template <int FMT, bool GATED, int NB>
+qlora_status_t launch_narrow_t(const NarrowParams& p, unsigned grid, cudaStream_t st) {
+  const size_t smem = narrow::smem_bytes(NB);
+  auto kern = qlora_narrow_kernel<FMT, GATED, NB>;
+  if (!set_smem(kern, smem)) return QLORA_ERR_CUDA;
+  LaunchScope scope(GATED ? kKindGatedFwd : kKindActFwd, st);
+  if (launch_pdl_cluster(kern, dim3(grid), dim3(narrow::kThreads), smem, st, p, unsigned(p.S)) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+template <bool GATED, int NB>
+qlora_status_t launch_narrow_f(int fmt, const NarrowParams& p, unsigned grid, cudaStream_t st) {
+  switch (fmt) {
+    case QLORA_FMT_NF4: return launch_narrow_t<kFmtNF4, GATED, NB>(p, grid, st);
+    case QLORA_FMT_MXFP4: return launch_narrow_t<kFmtMXFP4, GATED, NB>(p, grid, st);
+    case QLORA_FMT_NVFP4: return launch_narrow_t<kFmtNVFP4, GATED, NB>(p, grid, st);
+    default: return launch_narrow_t<kFmtNF4DQ, GATED, NB>(p, grid, st);
+  }
+}
+
+NarrowWeight narrow_weight(const qlora_weight_t* W, const void* B) {
+  return NarrowWeight{W->codes, W->scales, W->fmt == QLORA_FMT_NF4_DQ ? W->scales2 : nullptr,
+                      W->fmt == QLORA_FMT_NVFP4 ? W->tensor_scale : nullptr,
+                      static_cast<const __nv_bfloat16*>(B)};
+}
+
+// Blocks of 8 batch rows, as the kernels are compiled for.
+int narrow_blocks(int64_t M) { return M <= 8 ? 1 : (M <= 16 ? 2 : (M <= 32 ? 4 : 8)); }
+
+// T [nw][M, r] and Zs [M, nw r] of one or two adapters (Wu, Au null: one).
+qlora_status_t narrow_down(const qlora_weight_t* Wg, const qlora_weight_t* Wu, const void* X, const void* Ag,
+                           const void* Au, void* T, void* Zs, int64_t M, int r, float scale, cudaStream_t st) {
+  const int64_t K = Wg->K;
+  const int nw = Wu ? 2 : 1, nb = narrow_blocks(M);
+  NarrowDownParams d{};
+  d.a0 = static_cast<const __nv_bfloat16*>(Ag);
+  d.a1 = static_cast<const __nv_bfloat16*>(Au);
+  d.x = static_cast<const __nv_bfloat16*>(X);
+  d.ts0 = ts_of(Wg);
+  d.ts1 = Wu ? ts_of(Wu) : nullptr;
+  d.t = static_cast<__nv_bfloat16*>(T);
+  d.zs = static_cast<__nv_bfloat16*>(Zs);
+  d.M = int(M);
+  d.K = int(K);
+  d.r = r;
+  d.nw = nw;
+  d.ldzs = nw * r;
+  d.S = K >= 8192 ? 8 : (K >= 2048 ? 4 : 1);
+  d.s = scale;
+  d.zs_mul = short_zs_mul(Wg);
+  const unsigned groups = unsigned((nw * r + 15) / 16);
+  return nb == 1 ? launch_narrow_down_t<1>(d, groups, st)
+       : nb == 2 ? launch_narrow_down_t<2>(d, groups, st)
+       : nb == 4 ? launch_narrow_down_t<4>(d, groups, st)
+                 : launch_narrow_down_t<8>(d, groups, st);
+}
+
+// T and Zs by the kernels of the batch size: in the forward, and in a backward call that was not
+// given T (the forward's T bit for bit).
+qlora_status_t project_t(const qlora_weight_t* Wg, const qlora_weight_t* Wu, const void* X, const void* Ag,
+                           const void* Au, uint8_t* T, uint8_t* Zs, int64_t M, int r, float scale, void* ws,
+                           cudaStream_t s) {
+  if (M <= narrow::kMaxRows) return narrow_down(Wg, Wu, X, Ag, Au, T, Zs, M, r, scale, s);
+  const int nw = Wu ? 2 : 1;
+  for (int i = 0; i < nw; ++i) {
+    const qlora_status_t st = launch_lora_down(
+        false, X, M, Wg->K, i ? Au : Ag, r, scale, ts_of(i ? Wu : Wg), T + size_t(i) * M * r * 2,
+        Zs + size_t(i) * r * 2, ws_status(ws), nullptr, 1, false, kDownCtasBesidePair, s, 1.0f, 0, nullptr,
+        nullptr, nw * r);
+    if (st != QLORA_OK) return st;
+  }
+  return QLORA_OK;
+}
+
+// The whole forward of a batch of at most 64 rows (Wu: the up weight of a gated MLP, else null).  p
+// holds the epilogue's members; T [nw][M, r] and Zs [M, nw r] are written first.
+qlora_status_t run_narrow(const qlora_weight_t* Wg, const qlora_weight_t* Wu, const void* X, const void* Ag,
+                          const void* Bg, const void* Au, const void* Bu, void* T, void* Zs, int64_t M, int r,
+                          float scale, NarrowParams p, cudaStream_t st) {
+  const int64_t N = Wg->N, K = Wg->K;
+  const int nw = Wu ? 2 : 1;
+  const int nb = narrow_blocks(M);
+  const float zs_mul = short_zs_mul(Wg);
+  qlora_status_t rc = narrow_down(Wg, Wu, X, Ag, Au, T, Zs, M, r, scale, st);
+  if (rc != QLORA_OK) return rc;
+  p.w[0] = narrow_weight(Wg, Bg);
+  if (Wu) p.w[1] = narrow_weight(Wu, Bu);
+  p.x = static_cast<const __nv_bfloat16*>(X);
+  p.zs = static_cast<const __nv_bfloat16*>(Zs);
+  p.M = int(M);
+  p.N = int(N);
+  p.K = int(K);
+  p.r = r;
+  p.ldzs = nw * r;
+  const int cols = Wu ? narrow::kRows / 2 : narrow::kRows;
+  p.tiles = int((N + cols - 1) / cols);
+  p.chunks = int((K + narrow::CK - 1) / narrow::CK);
+  p.ts_mul = 1.0f / zs_mul;
+  p.one = 1u;
+  p.wide = (reinterpret_cast<uintptr_t>(p.w[0].codes) & 31u) == 0 &&
+           (!Wu || (reinterpret_cast<uintptr_t>(p.w[1].codes) & 31u) == 0);
+  // The split of a tile's depth over S CTAs that leaves the busiest CTA the fewest chunks (ties: the
+  // smaller S); every split costs about half a chunk in the sums that cross the cluster.
+  const int sms = num_sms();
+  double best = 1e30;
+  for (int S = 1; S <= narrow::kMaxSplit && S <= p.chunks; ++S) {
+    const int clusters = sms / S;
+    if (clusters < 1) break;
+    const double rounds = double((p.tiles + clusters - 1) / clusters);
+    const double cost = rounds * ((p.chunks + S - 1) / S + (S > 1 ? 0.5 : 0.25));
+    if (cost < best) {
+      best = cost;
+      p.S = S;
+    }
+  }
+  const int clusters = std::min(p.tiles, sms / p.S);
+  const unsigned grid = unsigned(clusters * p.S);
+  if (Wu) {
+    switch (nb) {
+      case 1: return launch_narrow_f<true, 1>(Wg->fmt, p, grid, st);
+      case 2: return launch_narrow_f<true, 2>(Wg->fmt, p, grid, st);
+      case 4: return launch_narrow_f<true, 4>(Wg->fmt, p, grid, st);
+      default: return launch_narrow_f<true, 8>(Wg->fmt, p, grid, st);
+    }
+  }
+  switch (nb) {
+    case 1: return launch_narrow_f<false, 1>(Wg->fmt, p, grid, st);
+    case 2: return launch_narrow_f<false, 2>(Wg->fmt, p, grid, st);
+    case 4: return launch_narrow_f<false, 4>(Wg->fmt, p, grid, st);
+    default: return launch_narrow_f<false, 8>(Wg->fmt, p, grid, st);
+  }
+}
+
 qlora_status_t check_gated(const qlora_weight_t* Wg, const qlora_weight_t* Wu, int act, int64_t M, int r) {
   qlora_status_t st = check_common(Wg, M, r);
   if (st != QLORA_OK) return st;
@@ -156,9 +305,6 @@ qlora_status_t check_gated(const qlora_weight_t* Wg, const qlora_weight_t* Wu, i
   return Wg->fmt == Wu->fmt ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
 }
 
-const float* ts_of(const qlora_weight_t* W) {
-  return W->fmt == QLORA_FMT_NVFP4 ? W->tensor_scale : nullptr;
-}
 
 }  // namespace
 }  // namespace qlora
@@ -181,13 +327,16 @@ qlora_status_t qlora_gated_mlp_fwd(const qlora_weight_t* Wg, const qlora_weight_
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(ws);
   uint8_t* T = T_save ? static_cast<uint8_t*>(T_save) : w + L.t;
-  const size_t mr = size_t(M) * size_t(r) * 2;
-  for (int i = 0; i < 2; ++i) {
-    st = launch_lora_down(false, X, M, Wg->K, i ? Au : Ag, r, scale, ts_of(i ? Wu : Wg), T + i * mr,
-                          w + L.zs + size_t(i) * r * 2, ws_status(ws), nullptr, 1, false,
-                          kDownCtasBesidePair, s, 1.0f, 0, nullptr, nullptr, 2 * r);
-    if (st != QLORA_OK) return st;
+  if (M <= narrow::kMaxRows) {
+    NarrowParams p{};
+    p.out = static_cast<__nv_bfloat16*>(H);
+    p.save0 = static_cast<__nv_bfloat16*>(G);
+    p.save1 = static_cast<__nv_bfloat16*>(U);
+    p.act = act;
+    return run_narrow(Wg, Wu, X, Ag, Bg, Au, Bu, T, w + L.zs, M, r, scale, p, s);
   }
+  st = project_t(Wg, Wu, X, Ag, Au, T, w + L.zs, M, r, scale, ws, s);
+  if (st != QLORA_OK) return st;
   FusedExParams p{};
   int grid = 0;
   st = fill_fused(p, Wg, false, X, w + L.zs, 2 * r, Bg, H, M, r, fused::HN, ws_status(ws), grid);
@@ -230,12 +379,8 @@ qlora_status_t qlora_gated_mlp_bwd(const qlora_weight_t* Wg, const qlora_weight_
   const size_t mr = size_t(M) * size_t(r) * 2, mn = size_t(M) * size_t(N) * 2;
   const uint8_t* Ts = static_cast<const uint8_t*>(T);
   if (!T) {   // recomputed with the forward's plan: the forward's T bit for bit
-    for (int i = 0; i < 2; ++i) {
-      st = launch_lora_down(false, X, M, K, i ? Au : Ag, r, scale, ts_of(i ? Wu : Wg), w + L.t + i * mr,
-                            w + L.zs + size_t(i) * r * 2, ws_status(ws), nullptr, 1, false,
-                            kDownCtasBesidePair, s, 1.0f, 0, nullptr, nullptr, 2 * r);
-      if (st != QLORA_OK) return st;
-    }
+    st = project_t(Wg, Wu, X, Ag, Au, w + L.t, w + L.zs, M, r, scale, ws, s);
+    if (st != QLORA_OK) return st;
     Ts = w + L.t;
   }
   void* const grad[2] = {w + L.grad, w + L.grad + mn};
@@ -283,8 +428,17 @@ qlora_status_t qlora_linear_act_fwd(const qlora_weight_t* W, const void* X, cons
   if (M == 0) return QLORA_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  st = launch_lora_down(false, X, M, W->K, A, r, scale, ts_of(W), T_save ? T_save : w + L.t, w + L.zs,
-                        ws_status(ws), nullptr, 1, false, kDownCtasBesidePair, s);
+  if (M <= narrow::kMaxRows) {
+    NarrowParams p{};
+    p.out = static_cast<__nv_bfloat16*>(Y);
+    p.save0 = static_cast<__nv_bfloat16*>(Z_save);
+    p.bias = static_cast<const __nv_bfloat16*>(bias);
+    p.residual = static_cast<const __nv_bfloat16*>(residual);
+    p.act = act;
+    return run_narrow(W, nullptr, X, A, B, nullptr, nullptr, T_save ? T_save : w + L.t, w + L.zs, M, r, scale, p, s);
+  }
+  st = project_t(W, nullptr, X, A, nullptr, T_save ? static_cast<uint8_t*>(T_save) : w + L.t, w + L.zs, M, r,
+                   scale, ws, s);
   if (st != QLORA_OK) return st;
   FusedExParams p{};
   int grid = 0;
@@ -327,8 +481,7 @@ qlora_status_t qlora_linear_act_bwd(const qlora_weight_t* W, const void* X, cons
   const bool short_dx = dX && short_fits(W, M, 1, true, region);
   const bool stream_dx = dX && !short_dx && stream_fits(W, M, 1, true, region);
   if (!T) {
-    st = launch_lora_down(false, X, M, K, A, r, scale, ts_of(W), w + L.t, w + L.zs, ws_status(ws), nullptr,
-                          1, false, kDownCtasBesidePair, s);
+    st = project_t(W, nullptr, X, A, nullptr, w + L.t, w + L.zs, M, r, scale, ws, s);
     if (st != QLORA_OK) return st;
     T = w + L.t;
   }

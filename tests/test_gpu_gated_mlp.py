@@ -12,7 +12,8 @@ BF = torch.bfloat16
 # rows from one to several tiles; columns and depth ragged against every tile (128, 256 and 64 wide)
 SHAPES = [(1, 16, 64, 8), (1, 272, 192, 16), (2, 4096, 256, 64), (7, 208, 448, 64), (33, 512, 1024, 32),
           (64, 336, 768, 8), (65, 400, 320, 16), (256, 528, 256, 64), (257, 272, 512, 32), (517, 1040, 576, 64),
-          (1030, 528, 256, 16), (600, 144, 4096, 64)]
+          (1030, 528, 256, 16), (600, 144, 4096, 64),
+          (1, 2064, 2112, 64), (9, 144, 1088, 32), (16, 1296, 8256, 8), (24, 160, 448, 64), (5, 20000, 192, 8)]
 FMTS = ("nf4", "mxfp4", "nvfp4", "nf4dq")
 
 

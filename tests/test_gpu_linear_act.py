@@ -11,7 +11,8 @@ from gpu_util import assert_close, to_f64
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
 SHAPES = [(1, 16, 64, 8), (1, 272, 1856, 16), (3, 4096, 256, 64), (20, 208, 448, 64), (64, 336, 768, 8),
-          (65, 400, 320, 16), (256, 528, 256, 64), (257, 272, 512, 32), (517, 1040, 576, 64), (1030, 528, 256, 16)]
+          (65, 400, 320, 16), (256, 528, 256, 64), (257, 272, 512, 32), (517, 1040, 576, 64), (1030, 528, 256, 16),
+          (1, 2064, 2112, 64), (9, 144, 1088, 32), (16, 1296, 8256, 8), (40, 160, 448, 64), (5, 40000, 192, 8)]
 FMTS = ("nf4", "mxfp4", "nvfp4", "nf4dq")
 
 
