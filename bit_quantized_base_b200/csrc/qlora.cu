@@ -516,8 +516,10 @@ qlora_status_t launch_fused_t(const FusedParams& p, int grid, bool grouped, cuda
 // W: one weight (E = 1) or E stacked weights; lora_up: B [E, N, r] (forward) or A [E, r, K] (dX).
 qlora_status_t launch_fused(const qlora_weight_t* W, bool dx, const void* act, const void* zs,
                             const void* lora_up, void* out, int64_t M, int r, int* status,
-                            const int32_t* offsets, int E, bool grouped, cudaStream_t st) {
+                            const int32_t* offsets, int E, bool grouped, cudaStream_t st,
+                            bool act_late = false) {
   FusedParams p{};
+  p.act_late = act_late ? 1 : 0;
   const int64_t N = W->N, K = W->K;
   const int64_t Kc = dx ? N : K;
   if (!tmap_2d(&p.tm_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, uint64_t(Kc), uint64_t(M),
@@ -591,12 +593,14 @@ qlora_status_t launch_stream_t(const StreamParams& p, int grid, cudaStream_t st)
 // the streaming kernel writes fp32 partials into `partial`, the reduce kernel writes `out`.
 qlora_status_t launch_stream(const qlora_weight_t* W, bool dx, const void* act, const void* zs,
                              const void* lora_up, void* out, int64_t M, int r, int* status,
-                             float* partial, size_t partial_bytes, cudaStream_t st) {
+                             float* partial, size_t partial_bytes, cudaStream_t st,
+                             bool act_late = false) {
   const int64_t N = W->N, K = W->K;
   const int64_t Kc = dx ? N : K;
   const StreamPlan sp = stream_plan(N, K, M, dx, num_sms());
   if (sp.partial_bytes > partial_bytes) return QLORA_ERR_WORKSPACE;
   StreamParams p{};
+  p.act_late = act_late ? 1 : 0;
   p.xrows = int((M + 15) / 16 * 16);
   const int mt = p.xrows <= 128 ? 1 : 2;
   if (!tmap_2d(&p.tm_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, uint64_t(Kc), uint64_t(M),
@@ -683,12 +687,14 @@ qlora_status_t launch_short_t(const ShortParams& p, int grid, cudaStream_t st) {
 // Zs written by lora_down with zs_mul = short_zs_mul(W)).
 qlora_status_t launch_short(const qlora_weight_t* W, bool dx, const void* act, const void* zs,
                             const void* lora_up, void* out, int64_t M, int r, void* ws,
-                            float* partial, size_t partial_bytes, cudaStream_t st) {
+                            float* partial, size_t partial_bytes, cudaStream_t st,
+                            bool act_late = false) {
   const int64_t N = W->N, K = W->K;
   const int64_t Kc = dx ? N : K;
   const ShortPlan sp = short_plan(N, K, M, dx, num_sms());
   if (sp.partial_bytes > partial_bytes || sp.tiles > shortk::kMaxTiles) return QLORA_ERR_WORKSPACE;
   ShortParams p{};
+  p.act_late = act_late ? 1 : 0;
   p.xrows = int((M + 15) / 16 * 16);
   if (!tmap_2d(&p.tm_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, uint64_t(Kc), uint64_t(M),
                uint64_t(Kc) * 2, 64, uint32_t(p.xrows), CU_TENSOR_MAP_SWIZZLE_128B))

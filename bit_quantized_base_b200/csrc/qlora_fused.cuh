@@ -106,6 +106,7 @@ struct FusedParams {
   int num_n, num_k;                  // pair tiles over output columns; contraction steps
   int tail_split;                    // the last tail_split 512-row tiles run as 2 x 256-row tiles
   uint32_t zero;                     // 0 (see zero_after)
+  int act_late;                      // the activations come from the previous kernel: wait for it first
 };
 
 enum : int { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2 };
@@ -355,7 +356,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
         for (int ks = 0; ks < nt; ++ks, ++i) {
           const uint32_t sx = i % NS, px = (i / NS) & 1u;
           if (!ptx::mbar_wait(empty_s(sx), px ^ 1u, p.status, abort_flag)) { ok = false; break; }
-          if (ks == nk && !waited) {
+          if ((ks == nk || p.act_late) && !waited) {
             ptx::griddep_wait();
             waited = true;
           }

@@ -152,12 +152,13 @@ qlora_status_t fork_join(cudaStream_t s, F&& side_work, G&& main_work) {
   return st;
 }
 
-// ------------------------------------------------------------------------- batches of up to 64 rows
+// ------------------------------------------------------------------------- batches of up to 16 rows
 template <int NB>
 qlora_status_t launch_narrow_down_t(const NarrowDownParams& p, unsigned groups, cudaStream_t st) {
   if (!set_smem(qlora_narrow_down_kernel<NB>, 0)) return QLORA_ERR_CUDA;
   LaunchScope scope(kKindNarrowDown, st);
-  if (launch_pdl_cluster(qlora_narrow_down_kernel<NB>, dim3(groups * unsigned(p.S)), dim3(narrow::kThreads), 0,
+  if (launch_pdl_cluster(qlora_narrow_down_kernel<NB>, dim3(groups * unsigned(p.S)),
+                         dim3(narrow::kDownWarps * 32), 0,
                          st, p, unsigned(p.S)) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
@@ -169,8 +170,7 @@ qlora_status_t launch_narrow_t(const NarrowParams& p, unsigned grid, cudaStream_
   auto kern = qlora_narrow_kernel<FMT, GATED, NB>;
   if (!set_smem(kern, smem)) return QLORA_ERR_CUDA;
   LaunchScope scope(GATED ? kKindGatedFwd : kKindActFwd, st);
-  if (launch_pdl_cluster(kern, dim3(grid), dim3(narrow::kThreads), smem, st, p, unsigned(p.S)) != cudaSuccess)
-    return QLORA_ERR_CUDA;
+  if (launch_pdl(kern, dim3(grid), dim3(narrow::kThreads), smem, st, p) != cudaSuccess) return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
@@ -191,7 +191,7 @@ NarrowWeight narrow_weight(const qlora_weight_t* W, const void* B) {
 }
 
 // Blocks of 8 batch rows, as the kernels are compiled for.
-int narrow_blocks(int64_t M) { return M <= 8 ? 1 : (M <= 16 ? 2 : (M <= 32 ? 4 : 8)); }
+int narrow_blocks(int64_t M) { return M <= 8 ? 1 : 2; }
 
 // T [nw][M, r] and Zs [M, nw r] of one or two adapters (Wu, Au null: one).
 qlora_status_t narrow_down(const qlora_weight_t* Wg, const qlora_weight_t* Wu, const void* X, const void* Ag,
@@ -213,12 +213,9 @@ qlora_status_t narrow_down(const qlora_weight_t* Wg, const qlora_weight_t* Wu, c
   d.ldzs = nw * r;
   d.S = K >= 8192 ? 8 : (K >= 2048 ? 4 : 1);
   d.s = scale;
-  d.zs_mul = short_zs_mul(Wg);
+  d.zs_mul = 1.0f;
   const unsigned groups = unsigned((nw * r + 15) / 16);
-  return nb == 1 ? launch_narrow_down_t<1>(d, groups, st)
-       : nb == 2 ? launch_narrow_down_t<2>(d, groups, st)
-       : nb == 4 ? launch_narrow_down_t<4>(d, groups, st)
-                 : launch_narrow_down_t<8>(d, groups, st);
+  return nb == 1 ? launch_narrow_down_t<1>(d, groups, st) : launch_narrow_down_t<2>(d, groups, st);
 }
 
 // T and Zs by the kernels of the batch size: in the forward, and in a backward call that was not
@@ -238,15 +235,15 @@ qlora_status_t project_t(const qlora_weight_t* Wg, const qlora_weight_t* Wu, con
   return QLORA_OK;
 }
 
-// The whole forward of a batch of at most 64 rows (Wu: the up weight of a gated MLP, else null).  p
+// The whole forward of a batch of at most 16 rows (Wu: the up weight of a gated MLP, else null).  p
 // holds the epilogue's members; T [nw][M, r] and Zs [M, nw r] are written first.
 qlora_status_t run_narrow(const qlora_weight_t* Wg, const qlora_weight_t* Wu, const void* X, const void* Ag,
                           const void* Bg, const void* Au, const void* Bu, void* T, void* Zs, int64_t M, int r,
-                          float scale, NarrowParams p, cudaStream_t st) {
+                          float scale, NarrowParams p, void* ws, float* partial, size_t partial_bytes,
+                          cudaStream_t st) {
   const int64_t N = Wg->N, K = Wg->K;
   const int nw = Wu ? 2 : 1;
   const int nb = narrow_blocks(M);
-  const float zs_mul = short_zs_mul(Wg);
   qlora_status_t rc = narrow_down(Wg, Wu, X, Ag, Au, T, Zs, M, r, scale, st);
   if (rc != QLORA_OK) return rc;
   p.w[0] = narrow_weight(Wg, Bg);
@@ -261,40 +258,20 @@ qlora_status_t run_narrow(const qlora_weight_t* Wg, const qlora_weight_t* Wu, co
   const int cols = Wu ? narrow::kRows / 2 : narrow::kRows;
   p.tiles = int((N + cols - 1) / cols);
   p.chunks = int((K + narrow::CK - 1) / narrow::CK);
-  p.ts_mul = 1.0f / zs_mul;
-  p.one = 1u;
-  p.wide = (reinterpret_cast<uintptr_t>(p.w[0].codes) & 31u) == 0 &&
-           (!Wu || (reinterpret_cast<uintptr_t>(p.w[1].codes) & 31u) == 0);
-  // The split of a tile's depth over S CTAs that leaves the busiest CTA the fewest chunks (ties: the
-  // smaller S); every split costs about half a chunk in the sums that cross the cluster.
-  const int sms = num_sms();
-  double best = 1e30;
-  for (int S = 1; S <= narrow::kMaxSplit && S <= p.chunks; ++S) {
-    const int clusters = sms / S;
-    if (clusters < 1) break;
-    const double rounds = double((p.tiles + clusters - 1) / clusters);
-    const double cost = rounds * ((p.chunks + S - 1) / S + (S > 1 ? 0.5 : 0.25));
-    if (cost < best) {
-      best = cost;
-      p.S = S;
-    }
-  }
-  const int clusters = std::min(p.tiles, sms / p.S);
-  const unsigned grid = unsigned(clusters * p.S);
-  if (Wu) {
-    switch (nb) {
-      case 1: return launch_narrow_f<true, 1>(Wg->fmt, p, grid, st);
-      case 2: return launch_narrow_f<true, 2>(Wg->fmt, p, grid, st);
-      case 4: return launch_narrow_f<true, 4>(Wg->fmt, p, grid, st);
-      default: return launch_narrow_f<true, 8>(Wg->fmt, p, grid, st);
-    }
-  }
-  switch (nb) {
-    case 1: return launch_narrow_f<false, 1>(Wg->fmt, p, grid, st);
-    case 2: return launch_narrow_f<false, 2>(Wg->fmt, p, grid, st);
-    case 4: return launch_narrow_f<false, 4>(Wg->fmt, p, grid, st);
-    default: return launch_narrow_f<false, 8>(Wg->fmt, p, grid, st);
-  }
+  // Equal ranges of (tile, chunk) units over the SMs; without room for the partials, or with more
+  // tiles than counters, whole tiles.
+  p.status = ws_status(ws);
+  p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + kCounterOffset);
+  p.partial = partial;
+  const int64_t sms = num_sms(), units = int64_t(p.tiles) * p.chunks;
+  const bool split = p.tiles <= narrow::kMaxCounters && partial_bytes >= narrow_partial_bytes(M, sms);
+  const int64_t iters = split ? (units + sms - 1) / sms : (p.tiles + sms - 1) / sms * p.chunks;
+  if (units > INT32_MAX) return QLORA_ERR_UNSUPPORTED;
+  p.iters = int(iters);
+  const unsigned grid = unsigned((units + iters - 1) / iters);
+  if (Wu)
+    return nb == 1 ? launch_narrow_f<true, 1>(Wg->fmt, p, grid, st) : launch_narrow_f<true, 2>(Wg->fmt, p, grid, st);
+  return nb == 1 ? launch_narrow_f<false, 1>(Wg->fmt, p, grid, st) : launch_narrow_f<false, 2>(Wg->fmt, p, grid, st);
 }
 
 qlora_status_t check_gated(const qlora_weight_t* Wg, const qlora_weight_t* Wu, int act, int64_t M, int r) {
@@ -333,7 +310,8 @@ qlora_status_t qlora_gated_mlp_fwd(const qlora_weight_t* Wg, const qlora_weight_
     p.save0 = static_cast<__nv_bfloat16*>(G);
     p.save1 = static_cast<__nv_bfloat16*>(U);
     p.act = act;
-    return run_narrow(Wg, Wu, X, Ag, Bg, Au, Bu, T, w + L.zs, M, r, scale, p, s);
+    return run_narrow(Wg, Wu, X, Ag, Bg, Au, Bu, T, w + L.zs, M, r, scale, p, ws,
+                      reinterpret_cast<float*>(w + L.partial), ws_bytes - L.partial, s);
   }
   st = project_t(Wg, Wu, X, Ag, Au, T, w + L.zs, M, r, scale, ws, s);
   if (st != QLORA_OK) return st;
@@ -410,6 +388,7 @@ qlora_status_t qlora_gated_mlp_bwd(const qlora_weight_t* Wg, const qlora_weight_
     p.scales_up = Wu->scales;
     p.scales2_up = Wu->scales2;
     p.lora_up_up = static_cast<const __nv_bfloat16*>(Au);
+    p.act_late = 1;                          // dG and dU are the kernel before's
     return launch_fused_ex<true, kEpiGated>(Wg->fmt, p, grid, s);
   });
 }
@@ -435,7 +414,8 @@ qlora_status_t qlora_linear_act_fwd(const qlora_weight_t* W, const void* X, cons
     p.bias = static_cast<const __nv_bfloat16*>(bias);
     p.residual = static_cast<const __nv_bfloat16*>(residual);
     p.act = act;
-    return run_narrow(W, nullptr, X, A, B, nullptr, nullptr, T_save ? T_save : w + L.t, w + L.zs, M, r, scale, p, s);
+    return run_narrow(W, nullptr, X, A, B, nullptr, nullptr, T_save ? T_save : w + L.t, w + L.zs, M, r, scale, p,
+                      ws, reinterpret_cast<float*>(w + L.partial), ws_bytes - L.partial, s);
   }
   st = project_t(W, nullptr, X, A, nullptr, T_save ? static_cast<uint8_t*>(T_save) : w + L.t, w + L.zs, M, r,
                    scale, ws, s);
@@ -506,9 +486,11 @@ qlora_status_t qlora_linear_act_bwd(const qlora_weight_t* W, const void* X, cons
   };
   if (!dX) return side_work(s);
   return fork_join(s, side_work, [&]() {
-    if (short_dx) return launch_short(W, true, dZ, w + L.zs, A, dX, M, r, ws, part, region, s);
-    if (stream_dx) return launch_stream(W, true, dZ, w + L.zs, A, dX, M, r, ws_status(ws), part, region, s);
-    return launch_fused(W, true, dZ, w + L.zs, A, dX, M, r, ws_status(ws), nullptr, 1, false, s);
+    const bool late = grad[0] != nullptr;    // dZ is the kernel before's
+    if (short_dx) return launch_short(W, true, dZ, w + L.zs, A, dX, M, r, ws, part, region, s, late);
+    if (stream_dx)
+      return launch_stream(W, true, dZ, w + L.zs, A, dX, M, r, ws_status(ws), part, region, s, late);
+    return launch_fused(W, true, dZ, w + L.zs, A, dX, M, r, ws_status(ws), nullptr, 1, false, s, late);
   });
 }
 

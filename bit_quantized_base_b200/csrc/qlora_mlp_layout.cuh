@@ -8,6 +8,11 @@ namespace {
 // n = 2 (gated) or 1 weights.  header | Zs [M, n r] | T [n][M, r] | backward: U [n][M, r],
 // gradients of the pre-activations [n][M, N] bf16, the projection's cluster sums, bias partials
 // [ceil(M/128)][N] fp32 (n = 1), and the short-batch kernels' fp32 partials.
+// fp32 partials of the narrow kernel (batches of up to 16 rows): two pieces per CTA.
+size_t narrow_partial_bytes(int64_t M, int64_t sms) {
+  return M > 0 && M <= narrow::kMaxRows ? size_t(sms) * 2 * narrow::partial_floats(int(M)) * 4 : 0;
+}
+
 struct MlpLayout {
   size_t zs, t, u, grad, sums, bias, partial, total;
 };
@@ -30,8 +35,8 @@ MlpLayout mlp_layout(int64_t N, int64_t K, int64_t M, int r, int n, bool bwd, in
     L.bias = take(n == 1 ? (m + 127) / 128 * size_t(N) * 4 : 0);
   }
   L.partial = off;
-  size_t pb = 0;
-  if (bwd && n == 1 && M > 0 && M <= shortk::kMaxRows) pb = short_plan(N, K, M, true, sms).partial_bytes;
+  size_t pb = narrow_partial_bytes(M, sms);
+  if (bwd && n == 1 && M > 0 && M <= shortk::kMaxRows) pb = std::max(pb, short_plan(N, K, M, true, sms).partial_bytes);
   if (bwd && n == 1 && use_stream(M, 1)) pb = std::max(pb, stream_plan(N, K, M, true, sms).partial_bytes);
   take(pb);
   L.total = off;

@@ -1,27 +1,42 @@
 // qlora_narrow.cuh -- forward of the gated MLP and of the linear layer with an epilogue for batches of
-// at most 64 rows (single tokens, decoding batches): each pass streams the 4-bit weights once.
+// at most 16 rows (single tokens, small decoding batches): each pass streams the 4-bit weights once.
 //
 //   qlora_narrow_down_kernel   T = X A^T of one or two adapters in one launch, and Zs = bf16(T s / ts)
 //   qlora_narrow_kernel        G and U, or Z, and the whole epilogue in one kernel
 //
 // What bounds it: reading the weights (one token of a 14336 x 4096 NF4 gate and up: 66 MB, 10 us) and
-// the SMs' decode (about 3 integer operations a weight, 20-30 weights a clock and SM).  Here a decoded
-// pair of weights goes from the register it was decoded in straight into a warp-level m16n8k16
-// tensor-core product (weights the 16-row operand, batch rows the 8 columns), with no barrier, copy
-// or hand-off between decode and product: the tcgen05 path has to place every decoded operand in
-// shared or tensor memory and synchronise with the issuing thread once per tile, which costs it half
-// of the decode rate at these batch sizes.  The warp product's own rate (about 1000 multiply-adds a
-// clock and SM) is above the decode's up to about 32 rows.
+// the SMs' decode.  A decoded pair of weights goes from the register it was decoded in straight into a
+// warp-level m16n8k16 tensor-core product (weights the 16-row operand, batch rows the 8 columns), with
+// no copy or hand-off between decode and product: the tcgen05 path has to place every decoded operand
+// in shared or tensor memory and synchronise with the issuing thread.  The warp product's rate sets
+// the limit of 16 rows: measured 8 clocks a sub-partition, so 8 rows allow 128 weights a clock and SM,
+// but a decoded register serves only 8 rows per product.
+//
+// Decode: one code byte (two weights) indexes a 256-entry table in shared memory, replicated so that
+// every lane reads its own banks.  MXFP4 / NVFP4: the pair of E2M1 values in bf16, times the block's
+// scale in one packed multiply (exact).  NF4: the pair of levels in binary32, each times the absmax,
+// rounded to bf16 (the definition).  NF4's entries are 8 bytes, which makes the shared-memory reads
+// the limit (2 clocks a warp and pair), while the table-in-registers decode of qlora_dequant.cuh is
+// limited by the byte permutes (2 clocks each a sub-partition, measured, and 2.6 a weight); kNfRegWords
+// of every 8 words go the second way, which balances the two.
 //
 // The order of the contraction is free as long as both operands agree: lane t of a quad takes the
 // 64-element block 4 j + t of its two weight rows (32 contiguous code bytes, one block scale), and
-// step i of a block multiplies its elements 4 i .. 4 i + 3, so the operand registers are the decoded
-// pairs as they come, and the batch operand is a 16-byte piece of X for every two steps.
+// two steps of a block multiply 8 consecutive elements, so the operand registers are the decoded pairs
+// as they come, and the batch operand is a 16-byte piece of X for every two steps.
 //
-// Work split: a CTA (8 warps) owns 128 columns of the gate and of the up weight (gated; the two
-// accumulators of an output sit in the same thread) or 256 columns; S CTAs of a cluster share a
-// tile's depth in contiguous ranges of 256-deep chunks and add their sums in rank order through
-// distributed shared memory, each finishing a part of the outputs.  Deterministic.
+// Work split: a tile is 256 weight rows (gated: 128 of the gate and the same 128 of the up weight, one
+// row group of 16 per warp), a unit of work one 256-deep chunk of a tile.  The flat space of units is
+// cut into equal contiguous ranges, one per CTA and one CTA per SM.  A tile that one CTA covers is
+// finished from its shared memory; the pieces of a split tile go to fp32 partials in the workspace
+// and the CTA that counts in last adds them in piece order (deterministic) and finishes the tile.
+// (Splitting over clusters instead, with the sums in distributed shared memory, left SMs idle: only
+// 15 clusters of 8 or 33 of 4 fit beside each other on 148 SMs.)
+//
+// 20 warps, so that none waits for another's latency: 16 decode and multiply, each with its own ring
+// of code units (asynchronous copies, three units ahead, no barrier); 2 bring the chunks of X through a
+// ring that lets the decoding warps drift apart; 2 finish tiles (partials, arrival, epilogue) from one
+// of two fp32 tile buffers while the others go on with the next tile.
 #pragma once
 #include <cuda_bf16.h>
 #include "qlora_ptx.cuh"
@@ -31,18 +46,27 @@
 
 namespace qlora {
 namespace narrow {
-constexpr int kMaxRows = 64;
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kMaxRows = 16;
+constexpr int kWarps = 16;                 // decoding warps
+constexpr int kXWarps = 2;                 // warps that bring X, taking turns
+constexpr int kEpiWarps = 2;               // warps that finish tiles
+constexpr int kThreads = (kWarps + kXWarps + kEpiWarps) * 32;
 constexpr int CK = 256;                    // contraction elements of one chunk: 4 blocks of 64
-constexpr int NSTAGE = 3;                  // chunks of X in shared memory
-constexpr int RG = 2;                      // 16-row groups per warp (gated: one gate, one up)
-constexpr int kRows = kWarps * RG * 16;    // 256 weight rows per CTA tile
+constexpr int NX = 4;                      // chunks of X in shared memory
+constexpr int NC = 4;                      // units of codes in shared memory, per warp
+constexpr int C_BYTES = 16 * CK / 2;       // one unit's codes of a warp: 16 rows x 128 bytes
+constexpr int kRows = kWarps * 16;         // 256 weight rows per tile
 constexpr int ROWP = kRows + 4;            // pitch of the fp32 tile in shared memory (no conflicts)
-constexpr int kMaxSplit = 8;
-// bytes: X chunks (nb blocks of 8 batch rows), then the fp32 tile [8 nb][ROWP]
+constexpr int kDownWarps = 8;              // warps of a down-projection CTA
+constexpr int kMaxCounters = 1984;         // arrival counters in the workspace header, one per tile
+// fp32 partials: at most two pieces of split tiles per CTA, [8 nb rows][kRows] each
+__host__ __device__ constexpr size_t partial_floats(int M) { return size_t(M) * kRows; }
 __host__ __device__ constexpr size_t x_bytes(int nb) { return size_t(nb) * 8 * CK * 2; }
+constexpr int kTableBytes = 256 * 128;     // 256 entries x 32 lanes x 4 bytes, or x 16 lanes x 8
+constexpr int kNfRegWords = 3;             // NF4: words of each 8 decoded from registers
+// decode table, codes ring, X ring, two fp32 tiles [8 nb][ROWP], barriers
 __host__ __device__ constexpr size_t smem_bytes(int nb) {
-  return NSTAGE * x_bytes(nb) + size_t(nb) * 8 * ROWP * 4;
+  return kTableBytes + size_t(kWarps) * NC * C_BYTES + NX * x_bytes(nb) + size_t(2) * nb * 8 * ROWP * 4 + 256;
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -57,64 +81,108 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// The 32 code bytes of one block.  wide: the address is a multiple of 32.
-__device__ __forceinline__ void load_block(uint32_t (&w)[8], const uint8_t* p, bool wide) {
-  if (wide) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
+// Entry e of the decode table, of which lane `l` reads its own copy.
+template <int FMT>
+__device__ __forceinline__ void table_entry(uint32_t table, int e, int l) {
+  if constexpr (FMT == kFmtNF4 || FMT == kFmtNF4DQ) {
+    float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if ((e & 15) == i) lo = nf4_level_dev(i);
+      if ((e >> 4) == i) hi = nf4_level_dev(i);
+    }
+    if (l < 16)
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(table + uint32_t(e * 128 + l * 8)), "f"(lo), "f"(hi) : "memory");
   } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    uint32_t o[4];
+    e2m1_decode8(uint32_t(e), o);             // codes 0 and 1 of the word
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(table + uint32_t(e * 128 + l * 4)), "r"(o[0]) : "memory");
   }
 }
+// The shared-memory address of byte b's entry: lane_base + 128 * byte.
+__device__ __forceinline__ uint32_t entry_addr(uint32_t lane_base, uint32_t w, int b) {
+  uint32_t a;
+  asm("mad.lo.u32 %0, %1, 128, %2;" : "=r"(a) : "r"(ptx::prmt(w, 0u, 0x4440u + uint32_t(b))), "r"(lane_base));
+  return a;
+}
 
-// One 64-element block's decoder: its table (NF4) or packed scales, then 8 codes at a time.
+// One 64-element block's decoder: its scales, then 8 codes (a word) at a time into pairs 2 i, 2 i + 1.
 template <int FMT>
-struct BlockDecoder {
-  Lut16 lut;
-  __device__ __forceinline__ void init(uint32_t raw) { lut = nf4_lut(__uint_as_float(raw)); }
-  __device__ __forceinline__ void word(int, uint32_t w, const DecodeMul& k, uint32_t (&o)[4]) const {
-    nf4_lookup8_mul(lut, w, k, o);
+struct BlockDecoder {                         // NF4, NF4DQ
+  Lut16 t;
+  float absmax;
+  __device__ __forceinline__ static uint32_t lane_base(uint32_t table, int lane) {
+    return table + uint32_t(lane & 15) * 8u;
   }
-};
-// MXFP4: bit placement times 2^(e-1) for e <= 128, else in two exact multiplies (see qlora_dequant.cuh).
-template <>
-struct BlockDecoder<kFmtMXFP4> {
-  uint32_t s0, s1;
-  bool slow;
   __device__ __forceinline__ void init(uint32_t raw) {
-    const uint32_t e0 = raw & 0xFFu, e1 = (raw >> 8) & 0xFFu;
-    slow = e0 > 128u || e1 > 128u;
-    s0 = slow ? mx_exact_scale(e0) : mx_fast_scale(e0);
-    s1 = slow ? mx_exact_scale(e1) : mx_fast_scale(e1);
+    absmax = __uint_as_float(raw);
+    t = nf4_lut(absmax);
   }
-  __device__ __forceinline__ void word(int j, uint32_t w, const DecodeMul& k, uint32_t (&o)[4]) const {
-    e2m1_pattern8(w, k, o);
-    const uint32_t s = j < 4 ? s0 : s1;
-    if (slow) {
+  __device__ __forceinline__ void word(int j, uint32_t w, uint32_t base, uint32_t (&o)[4]) const {
+    if (j >= kNfRegWords) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = ptx::mul_bf16x2(o[i], kBf16x2Pow126);
+      for (int b = 0; b < 4; ++b) {
+        float lo, hi;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(lo), "=f"(hi) : "r"(entry_addr(base, w, b)));
+        o[b] = ptx::cvt_bf16x2(__fmul_rn(lo, absmax), __fmul_rn(hi, absmax));
+      }
+    } else {
+      // As lut16_lookup8, with the halves of the table chosen by a third permute whose selector is
+      // the identity plus 4 where the code is above 7.
+      const uint32_t sel3 = w & 0x77777777u;                        // low 3 bits of each code
+      const uint32_t pick = ((w >> 1) & 0x44444444u) | 0x32103210u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t s = h ? sel3 >> 16 : sel3, q = h ? pick >> 16 : pick;
+        const uint32_t lo = ptx::prmt(ptx::prmt(t.lo[0], t.lo[1], s), ptx::prmt(t.lo[2], t.lo[3], s), q);
+        const uint32_t hi = ptx::prmt(ptx::prmt(t.hi[0], t.hi[1], s), ptx::prmt(t.hi[2], t.hi[3], s), q);
+        o[2 * h] = ptx::prmt(lo, hi, 0x5140u);
+        o[2 * h + 1] = ptx::prmt(lo, hi, 0x7362u);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = ptx::mul_bf16x2(o[i], s);
   }
 };
-// NVFP4: elements times 2^-8 (the epilogue multiplies by 2^8 ts; Zs carries the same 2^-8).
-template <>
-struct BlockDecoder<kFmtNVFP4> {
-  uint32_t s[4];
+// MXFP4 and NVFP4: table pair times the block's scale, exact (at most 2 x 4 significant bits).
+template <int FMT>
+struct E2m1Decoder {
+  uint32_t s[4];                              // packed scale of words 2 q, 2 q + 1
+  __device__ __forceinline__ static uint32_t lane_base(uint32_t table, int lane) { return table + uint32_t(lane) * 4u; }
   __device__ __forceinline__ void init(uint32_t raw) {
+    if constexpr (FMT == kFmtMXFP4) {
+      s[0] = s[1] = mx_exact_scale(raw);
+      s[2] = s[3] = mx_exact_scale(raw >> 8);
+    } else {
+      // E4M3 to bf16, two at a time: exponent and mantissa placed in the low bits of the bf16 fields
+      // are the value times 2^-120 (E4M3's subnormals are bf16's there); a NaN byte takes the slow way
 #pragma unroll
-    for (int q = 0; q < 4; ++q) s[q] = nv_shifted_scale((raw >> (8 * q)) & 0xFFu);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = ptx::prmt(raw, 0u, h ? 0x4342u : 0x4140u);
+        const uint32_t v = ptx::mul_bf16x2(((x & 0x007F007Fu) << 4) | ((x & 0x00800080u) << 8), 0x7B807B80u);
+        s[2 * h] = ptx::prmt(v, 0u, 0x1010u);
+        s[2 * h + 1] = ptx::prmt(v, 0u, 0x3232u);
+      }
+      if ((((raw & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t v = e4m3_bf16(raw >> (8 * q));
+          s[q] = v | (v << 16);
+        }
+      }
+    }
   }
-  __device__ __forceinline__ void word(int j, uint32_t w, const DecodeMul& k, uint32_t (&o)[4]) const {
-    e2m1_pattern8(w, k, o);
+  __device__ __forceinline__ void word(int j, uint32_t w, uint32_t base, uint32_t (&o)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = ptx::mul_bf16x2(o[i], s[j >> 1]);
+    for (int b = 0; b < 4; ++b) {
+      uint32_t v;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(entry_addr(base, w, b)));
+      o[b] = ptx::mul_bf16x2(v, s[j >> 1]);
+    }
   }
 };
+template <>
+struct BlockDecoder<kFmtMXFP4> : E2m1Decoder<kFmtMXFP4> {};
+template <>
+struct BlockDecoder<kFmtNVFP4> : E2m1Decoder<kFmtNVFP4> {};
 }  // namespace narrow
 
 struct NarrowWeight {
@@ -129,219 +197,333 @@ struct NarrowParams {
   const __nv_bfloat16 *x, *zs;       // [M, K]; [M, ldzs], weight i at column i r
   const __nv_bfloat16 *bias, *residual;
   __nv_bfloat16 *out, *save0, *save1;
+  float* partial;                    // [gridDim.x][2][M][kRows]
+  unsigned* counters;                // [tiles], zero between launches (split tiles only)
+  int* status;
   int M, N, K, r, ldzs;
-  int tiles, chunks, S, act;
-  float ts_mul;                      // 2^8 for NVFP4, else 1
-  uint32_t one;                      // 1 (see decode_mul)
-  int wide;                          // codes are 32-byte aligned
+  int tiles, chunks, iters, act;     // iters: units per CTA
 };
 
 template <int FMT, bool GATED, int NB>
 __global__ void __launch_bounds__(narrow::kThreads, 1)
 qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
   using namespace narrow;
+  using Dec = BlockDecoder<FMT>;
   constexpr int COLS = GATED ? kRows / 2 : kRows;      // output columns of a tile
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t xs = ptx::smem_u32(smem);
-  float* tile = reinterpret_cast<float*>(smem + NSTAGE * x_bytes(NB));
+  const uint32_t table = ptx::smem_u32(smem);
+  const uint32_t cs = table + uint32_t(kTableBytes);
+  const uint32_t xs = cs + uint32_t(kWarps * NC * C_BYTES);
+  constexpr int TILE = NB * 8 * ROWP;                  // floats of one tile buffer
+  float* tiles = reinterpret_cast<float*>(smem + kTableBytes + kWarps * NC * C_BYTES + NX * x_bytes(NB));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + 2 * TILE);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * NX + 4);
+  volatile unsigned* s_last = reinterpret_cast<volatile unsigned*>(abort_flag + 1);
+  const uint32_t b0 = ptx::smem_u32(bars);
+  auto full = [&](uint32_t s) { return b0 + 8u * s; };
+  auto empty = [&](uint32_t s) { return b0 + 8u * (NX + s); };
+  auto tile_full = [&](uint32_t b) { return b0 + 8u * (2 * NX + b); };
+  auto tile_empty = [&](uint32_t b) { return b0 + 8u * (2 * NX + 2 + b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int rank = int(blockIdx.x) % p.S, cluster = int(blockIdx.x) / p.S, clusters = int(gridDim.x) / p.S;
-  const int c0 = int((long long)p.chunks * rank / p.S), c1 = int((long long)p.chunks * (rank + 1) / p.S);
+  const int total = p.tiles * p.chunks;
+  const int u0 = int(blockIdx.x) * p.iters, u1 = min(u0 + p.iters, total);
   const int blocks = p.K / 64;
-  const DecodeMul km = decode_mul(p.one);
-  ptx::griddep_launch_dependents();
-
-  // X chunk c into stage s: piece (nb, i, lane) = 8 elements of batch row 8 nb + lane / 4 at block
-  // 4 c + lane % 4, element 8 i -- the order in which the products read them
-  auto stage_x = [&](int c, int s) {
-#pragma unroll
-    for (int q = 0; q < NB; ++q) {
-      const int v = int(threadIdx.x) + q * kThreads;   // nb = q, i = warp
-      const int row = 8 * q + g, blk = 4 * c + t;
-      const bool ok = row < p.M && blk < blocks;
-      const __nv_bfloat16* src = p.x + (ok ? size_t(row) * p.K + size_t(blk) * 64 + warp * 8 : 0);
-      cp_async_16(xs + uint32_t(s) * uint32_t(x_bytes(NB)) + uint32_t(v) * 16u, src, ok ? 16u : 0u);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NX; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(empty(s), kWarps);
     }
-    ptx::cp_async_commit();
-  };
-  // Weight rows of this lane: groups q = 0, 1, rows g and g + 8 of each (h), clamped to the weight (a
-  // clamped row's results are dropped).
-  auto row_of = [&](int tl, int q, int h) {
-    const int n = GATED ? tl * COLS + warp * 16 + g + 8 * h : tl * COLS + warp * 32 + q * 16 + g + 8 * h;
-    return min(n, p.N - 1);
-  };
-  auto load_codes_of = [&](int tl, int c, uint32_t (&w)[RG][2][8], uint32_t (&sc)[RG][2]) {
-    const int blk = 4 * c + t;
-#pragma unroll
-    for (int q = 0; q < RG; ++q)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const NarrowWeight& W = p.w[GATED ? q : 0];
-        if (blk < blocks) {
-          const int n = row_of(tl, q, h);
-          load_block(w[q][h], W.codes + (size_t(n) * p.K + size_t(blk) * 64) / 2, p.wide != 0);
-          if constexpr (FMT == kFmtNF4DQ)
-            sc[q][h] = load_item_scale_dq(W.scales, W.scales2, 0, p.N, n, blk * 64, p.K).raw;
-          else
-            sc[q][h] = load_item_scale<FMT>(W.scales, n, blk * 64, p.K).raw;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[q][h][i] = 0u;
-          sc[q][h] = 0u;
-        }
-      }
-  };
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(tile_full(b), kWarps);
+      ptx::mbar_init(tile_empty(b), kEpiWarps);
+    }
+    *abort_flag = 0;
+    ptx::fence_mbarrier_init();
+  }
+  ptx::griddep_launch_dependents();
+  for (int e = warp; e < 256; e += kThreads / 32) table_entry<FMT>(table, e, lane);
+  __syncthreads();
 
-  uint32_t nw[RG][2][8], nsc[RG][2];
-  if (cluster < p.tiles && c0 < c1) load_codes_of(cluster, c0, nw, nsc);
-  for (int tl = cluster; tl < p.tiles; tl += clusters) {
-    float acc[RG][NB][4];
+  if (warp >= kWarps && warp < kWarps + kXWarps) {
+    // ------------------------------------------------------------------ X
+    // piece (b, i, lane) = 8 elements of batch row 8 b + lane / 4 at block 4 c + lane % 4, element 8 i
+    // -- the order in which the products read them; zeros past M and K
+    for (int n = warp - kWarps; u0 + n < u1; n += kXWarps) {
+      const uint32_t s = uint32_t(n) % NX, ph = (uint32_t(n) / NX) & 1u;
+      const int blk = 4 * ((u0 + n) % p.chunks) + t;
+      uint4 v[NB][8];
 #pragma unroll
-    for (int q = 0; q < RG; ++q)
+      for (int b = 0; b < NB; ++b) {
+        const int row = 8 * b + g;
+        const bool ok = row < p.M && blk < blocks;
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + size_t(ok ? row : 0) * p.K + size_t(ok ? blk : 0) * 64);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[b][i] = ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (!ptx::mbar_wait(empty(s), ph ^ 1u, p.status, abort_flag)) break;
+      const uint32_t at = xs + s * uint32_t(x_bytes(NB)) + uint32_t(lane) * 16u;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[q][b][i] = 0.0f;
-    for (int s = 0; s < NSTAGE - 1; ++s) {
-      if (c0 + s < c1) stage_x(c0 + s, s);
-      else ptx::cp_async_commit();
+        for (int i = 0; i < 8; ++i) {
+          const uint4 q = v[b][i];
+          ptx::st_shared_v4(at + uint32_t(b * 8 + i) * 512u, q.x, q.y, q.z, q.w);
+        }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full(s));
     }
-    for (int c = c0; c < c1; ++c) {
-      const int s = (c - c0) % NSTAGE;
-      uint32_t w[RG][2][8], sc[RG][2];
+    return;
+  }
+
+  if (warp >= kWarps + kXWarps) {
+    // ------------------------------------------------------------------ tiles
+    const int et = int(threadIdx.x) - (kWarps + kXWarps) * 32;
+    ptx::griddep_wait();
+    uint32_t nt = 0;
+    for (int u = u0; u < u1; ++nt) {
+      const int tl = u / p.chunks;
+      u = min((tl + 1) * p.chunks, u1);
+      ptx::mbar_wait_idle(tile_full(nt & 1u), (nt >> 1) & 1u, p.status, abort_flag);
+      const float* tile = tiles + (nt & 1u) * TILE;
+      // the CTAs that share this tile
+      const int first = (tl * p.chunks) / p.iters, last = (tl * p.chunks + p.chunks - 1) / p.iters;
+      const size_t piece = partial_floats(p.M);
+      bool finish = first == last && *abort_flag == 0;
+      if (first != last) {
+        float* mine = p.partial + (size_t(blockIdx.x) * 2 + (u0 / p.chunks == tl ? 0 : 1)) * piece;
+        for (int e = et; e < p.M * (kRows / 4); e += kEpiWarps * 32) {
+          const int m = e / (kRows / 4), q = e % (kRows / 4);
+          __stcg(reinterpret_cast<float4*>(mine) + e, *reinterpret_cast<const float4*>(tile + size_t(m) * ROWP + 4 * q));
+        }
+        __threadfence();
+        ptx::named_bar_sync(1, kEpiWarps * 32);
+        if (et == 0) {
+          const unsigned n = atomicAdd(p.counters + tl, 1u);
+          *s_last = n == unsigned(last - first) ? 1u : 0u;
+          if (*s_last) p.counters[tl] = 0u;   // every piece has counted: back to zero for the next launch
+        }
+        ptx::named_bar_sync(1, kEpiWarps * 32);
+        finish = *s_last != 0u && *abort_flag == 0;
+        if (finish) __threadfence();
+      }
+      if (finish) {
+        // 8 columns at a time: the pieces in order, then the epilogue
+        const float ts0 = p.w[0].tensor_scale ? __ldg(p.w[0].tensor_scale) : 1.0f;
+        const float ts1 = GATED && p.w[1].tensor_scale ? __ldg(p.w[1].tensor_scale) : 1.0f;
+        constexpr int G8 = COLS / 8;
+        for (int it = et; it < p.M * G8; it += kEpiWarps * 32) {
+          const int m = it / G8, cc = (it % G8) * 8, n = tl * COLS + cc;
+          if (n >= p.N) continue;
+          float v[GATED ? 2 : 1][8];
 #pragma unroll
-      for (int q = 0; q < RG; ++q)
+          for (int q = 0; q < (GATED ? 2 : 1); ++q) {
+            const int col = q * COLS + cc;
+            if (first == last) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[q][i] = tile[size_t(m) * ROWP + col + i];
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[q][i] = 0.0f;
+#pragma unroll 4
+              for (int k = first; k <= last; ++k) {
+                const float* src = p.partial + (size_t(k) * 2 + ((k * p.iters) / p.chunks == tl ? 0 : 1)) * piece +
+                                   size_t(m) * kRows + col;
+                const float4 a = __ldcg(reinterpret_cast<const float4*>(src)),
+                             b = __ldcg(reinterpret_cast<const float4*>(src) + 1);
+                v[q][0] += a.x; v[q][1] += a.y; v[q][2] += a.z; v[q][3] += a.w;
+                v[q][4] += b.x; v[q][5] += b.y; v[q][6] += b.z; v[q][7] += b.w;
+              }
+            }
+          }
+          const size_t o = size_t(m) * p.N + n;
+          auto put = [&](__nv_bfloat16* dst, const float (&y)[8]) {
+            *reinterpret_cast<uint4*>(dst + o) =
+                make_uint4(ptx::cvt_bf16x2(y[0], y[1]), ptx::cvt_bf16x2(y[2], y[3]), ptx::cvt_bf16x2(y[4], y[5]),
+                           ptx::cvt_bf16x2(y[6], y[7]));
+          };
+          uint32_t z[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[0][i] *= ts0;
+            if constexpr (GATED) v[1][i] *= ts1;
+            z[i] = __float_as_uint(v[0][i]);
+          }
+          if constexpr (!GATED) {
+            if (p.bias) act::add8(z, __ldg(reinterpret_cast<const uint4*>(p.bias + n)));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[0][i] = __uint_as_float(z[i]);
+          }
+          if (p.save0) put(p.save0, v[0]);
+          if constexpr (GATED) {
+            if (p.save1) put(p.save1, v[1]);
+          }
+          act::apply<8>(p.act, z);
+          if constexpr (!GATED) {
+            if (p.residual) act::add8(z, *reinterpret_cast<const uint4*>(p.residual + o));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[0][i] = GATED ? __uint_as_float(z[i]) * v[GATED ? 1 : 0][i] : __uint_as_float(z[i]);
+          put(p.out, v[0]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(tile_empty(nt & 1u));
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------------ decode and multiply
+  const uint32_t lane_table = Dec::lane_base(table, lane);
+  // this warp's weight and its first row in the tile's columns
+  const int wi = GATED && warp >= kWarps / 2 ? 1 : 0;
+  const uint8_t* codes = p.w[wi].codes;
+  const void* scales = p.w[wi].scales;
+  const float* scales2 = p.w[wi].scales2;
+  const __nv_bfloat16* lora_up = p.w[wi].lora_up;
+  const int wrow = (GATED ? warp % (kWarps / 2) : warp) * 16;
+  const uint32_t ring = cs + uint32_t(warp * NC * C_BYTES);
+  // Row j of the warp's group in tile tl, clamped to the weight (a clamped row's results are dropped).
+  auto row_of = [&](int tl, int j) { return min(tl * COLS + wrow + j, p.N - 1); };
+  // A unit's codes: 16 rows x 128 bytes, 16-byte piece q of row j at q ^ (j & 1), so that the two
+  // halves of a block read by 8 neighbouring lanes fall into different banks.
+  auto copy_codes = [&](int tl, int c, uint32_t st) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = 4 * k + (lane >> 3), q = lane & 7;
+      const int blk = 4 * c + (q >> 1);
+      const bool ok = blk < blocks;
+      const uint8_t* src = codes + (size_t(row_of(tl, j)) * p.K) / 2 + (ok ? size_t(c) * (CK / 2) + q * 16 : 0);
+      cp_async_16(ring + st * uint32_t(C_BYTES) + uint32_t(j * 128 + ((q ^ (j & 1)) << 4)), src, ok ? 16u : 0u);
+    }
+  };
+  auto scale_of = [&](int tl, int c, uint32_t (&sc)[2]) {
+    const int blk = 4 * c + t;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sc[h] = 0u;
+      if (blk < blocks) {
+        const int n = row_of(tl, g + 8 * h);
+        if constexpr (FMT == kFmtNF4DQ) sc[h] = load_item_scale_dq(scales, scales2, 0, p.N, n, blk * 64, p.K).raw;
+        else sc[h] = load_item_scale<FMT>(scales, n, blk * 64, p.K).raw;
+      }
+    }
+  };
+  // cursor of the unit whose codes are copied next, NC - 1 units ahead
+  int ptl = u0 / p.chunks, pc = u0 % p.chunks, pu = u0;
+  auto copy_next = [&]() {
+    if (pu < u1) copy_codes(ptl, pc, uint32_t(pu - u0) % NC);
+    ptx::cp_async_commit();
+    ++pu;
+    if (++pc == p.chunks) { pc = 0; ++ptl; }
+  };
+  int tl = u0 / p.chunks, c = u0 % p.chunks;
+  uint32_t sc[2], nsc[2];
+  scale_of(tl, c, sc);
+#pragma unroll
+  for (int q = 0; q < NC - 1; ++q) copy_next();
+  float acc[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
+  uint32_t xst = 0, xph = 0, nt = 0;
+  for (int u = u0; u < u1; ++u) {
+    const bool tile_done = c + 1 == p.chunks;
+    ptx::cp_async_wait<NC - 2>();
+    __syncwarp();
+    uint32_t w[2][8];
+    {
+      const uint32_t at = ring + (uint32_t(u - u0) % NC) * uint32_t(C_BYTES);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t j = uint32_t(g + 8 * h);
+          const uint4 v = ptx::ld_shared_v4(at + j * 128u + (((2u * t + q) ^ (j & 1u)) << 4));
+          w[h][4 * q] = v.x; w[h][4 * q + 1] = v.y; w[h][4 * q + 2] = v.z; w[h][4 * q + 3] = v.w;
+        }
+    }
+    // operands of the LoRA term, loaded a unit's work ahead (Zs is the kernel before's)
+    uint32_t la[4][2][2], lz[4][NB][2];
+    if (tile_done) {
+      ptx::griddep_wait();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int ka = 16 * k + 2 * t, kb = ka + 8;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[q][h][i] = nw[q][h][i];
-          sc[q][h] = nsc[q][h];
+          const __nv_bfloat16* br = lora_up + size_t(row_of(tl, g + 8 * h)) * p.r;
+          la[k][h][0] = ka < p.r ? __ldg(reinterpret_cast<const uint32_t*>(br + ka)) : 0u;
+          la[k][h][1] = kb < p.r ? __ldg(reinterpret_cast<const uint32_t*>(br + kb)) : 0u;
         }
-      if (c + 1 < c1) load_codes_of(tl, c + 1, nw, nsc);
-      else if (tl + clusters < p.tiles) load_codes_of(tl + clusters, c0, nw, nsc);
-      ptx::cp_async_wait<NSTAGE - 2>();
-      __syncthreads();                       // chunk c is in place; everyone is done with chunk c - 1
-      if (c + NSTAGE - 1 < c1) stage_x(c + NSTAGE - 1, (c - c0 + NSTAGE - 1) % NSTAGE);
-      else ptx::cp_async_commit();
-      BlockDecoder<FMT> dec[RG][2];
-#pragma unroll
-      for (int q = 0; q < RG; ++q)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) dec[q][h].init(sc[q][h]);
-      const uint32_t xb = xs + uint32_t(s) * uint32_t(x_bytes(NB)) + uint32_t(lane) * 16u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t a[RG][2][4];
-#pragma unroll
-        for (int q = 0; q < RG; ++q)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) dec[q][h].word(i, w[q][h][i], km, a[q][h]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const uint4 x = ptx::ld_shared_v4(xb + uint32_t(b * 8 + i) * 512u);
-#pragma unroll
-          for (int q = 0; q < RG; ++q) {
-            mma16816(acc[q][b], a[q][0][0], a[q][1][0], a[q][0][1], a[q][1][1], x.x, x.y);
-            mma16816(acc[q][b], a[q][0][2], a[q][1][2], a[q][0][3], a[q][1][3], x.z, x.w);
-          }
+          const int m = 8 * b + g;
+          const __nv_bfloat16* zr = p.zs + size_t(m) * p.ldzs + wi * p.r;
+          lz[k][b][0] = m < p.M && ka < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(zr + ka)) : 0u;
+          lz[k][b][1] = m < p.M && kb < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(zr + kb)) : 0u;
         }
       }
     }
-    // The LoRA term: rows of B times Zs, by the last rank (Zs comes from the kernel before).
-    ptx::griddep_wait();
-    if (rank == p.S - 1) {
-      for (int k = 0; k < p.r; k += 16) {
-        const int ka = k + 2 * t, kb = ka + 8;
+    Dec dec[2];
+    dec[0].init(sc[0]);
+    dec[1].init(sc[1]);
+    if (u + 1 < u1) scale_of(tile_done ? tl + 1 : tl, tile_done ? 0 : c + 1, nsc);
+    // (the stage written here was read one unit ago, by products that have been issued since)
+    copy_next();
+    ptx::mbar_wait(full(xst), xph, p.status, abort_flag);   // giving up is seen at the tile's end
+    const uint32_t xb = xs + xst * uint32_t(x_bytes(NB)) + uint32_t(lane) * 16u;
 #pragma unroll
-        for (int q = 0; q < RG; ++q) {
-          const NarrowWeight& W = p.w[GATED ? q : 0];
-          uint32_t a[2][2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const __nv_bfloat16* br = W.lora_up + size_t(row_of(tl, q, h)) * p.r;
-            a[h][0] = __ldg(reinterpret_cast<const uint32_t*>(br + ka));
-            a[h][1] = kb < p.r ? __ldg(reinterpret_cast<const uint32_t*>(br + kb)) : 0u;
-          }
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const int m = 8 * b + g;
-            const __nv_bfloat16* zr = p.zs + size_t(m) * p.ldzs + (GATED ? q * p.r : 0);
-            const uint32_t z0 = m < p.M ? __ldcg(reinterpret_cast<const uint32_t*>(zr + ka)) : 0u;
-            const uint32_t z1 = m < p.M && kb < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(zr + kb)) : 0u;
-            mma16816(acc[q][b], a[0][0], a[1][0], a[0][1], a[1][1], z0, z1);
-          }
-        }
-      }
-    }
-    // fp32 tile [batch row][weight row] (gated: 128 gate rows, then 128 up rows)
-#pragma unroll
-    for (int q = 0; q < RG; ++q) {
-      const int row = GATED ? q * COLS + warp * 16 + g : warp * 32 + q * 16 + g;
+    for (int i = 0; i < 8; ++i) {
+      uint32_t a[2][4];
+      dec[0].word(i, w[0][i], lane_table, a[0]);
+      dec[1].word(i, w[1][i], lane_table, a[1]);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        float* d = tile + size_t(8 * b + 2 * t) * ROWP + row;
-        d[0] = acc[q][b][0];
-        d[ROWP] = acc[q][b][1];
-        d[8] = acc[q][b][2];
-        d[ROWP + 8] = acc[q][b][3];
+        // (lanes past the batch read nothing: fewer shared-memory cycles)
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (8 * b + g < p.M) x = ptx::ld_shared_v4(xb + uint32_t(b * 8 + i) * 512u);
+        mma16816(acc[b], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+        mma16816(acc[b], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
       }
     }
-    if (p.S > 1) ptx::cluster_sync();
-    else __syncthreads();
-    // 8 columns at a time: the ranks' sums in rank order, then the epilogue
-    const float ts0 = (p.w[0].tensor_scale ? __ldg(p.w[0].tensor_scale) : 1.0f) * p.ts_mul;
-    const float ts1 = GATED ? (p.w[1].tensor_scale ? __ldg(p.w[1].tensor_scale) : 1.0f) * p.ts_mul : 1.0f;
-    const uint32_t tile_a = ptx::smem_u32(tile);
-    constexpr int G8 = COLS / 8;
-    for (int it = rank * kThreads + int(threadIdx.x); it < p.M * G8; it += p.S * kThreads) {
-      const int m = it / G8, cc = (it % G8) * 8, n = tl * COLS + cc;
-      if (n >= p.N) continue;
-      float v[GATED ? 2 : 1][8];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(empty(xst));
+    if (++xst == uint32_t(NX)) { xst = 0; xph ^= 1u; }
+    sc[0] = nsc[0];
+    sc[1] = nsc[1];
+    if (tile_done) {
+      // the LoRA term: rows of B times Zs
 #pragma unroll
-      for (int q = 0; q < (GATED ? 2 : 1); ++q) {
+      for (int k = 0; k < 4; ++k)
+        if (16 * k < p.r) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[q][i] = 0.0f;
-        const uint32_t off = tile_a + uint32_t(m * ROWP + q * COLS + cc) * 4u;
-        for (int k = 0; k < p.S; ++k) {
-          const uint32_t ra = p.S > 1 ? ptx::mapa(off, uint32_t(k)) : off;
-          const float4 a = ptx::ld_dsmem_f4(ra), b = ptx::ld_dsmem_f4(ra + 16u);
-          v[q][0] += a.x; v[q][1] += a.y; v[q][2] += a.z; v[q][3] += a.w;
-          v[q][4] += b.x; v[q][5] += b.y; v[q][6] += b.z; v[q][7] += b.w;
+          for (int b = 0; b < NB; ++b)
+            mma16816(acc[b], la[k][0][0], la[k][1][0], la[k][0][1], la[k][1][1], lz[k][b][0], lz[k][b][1]);
         }
-      }
-      const size_t o = size_t(m) * p.N + n;
-      auto put = [&](__nv_bfloat16* dst, const float (&y)[8]) {
-        *reinterpret_cast<uint4*>(dst + o) =
-            make_uint4(ptx::cvt_bf16x2(y[0], y[1]), ptx::cvt_bf16x2(y[2], y[3]), ptx::cvt_bf16x2(y[4], y[5]),
-                       ptx::cvt_bf16x2(y[6], y[7]));
-      };
-      uint32_t z[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[0][i] *= ts0;
-        if constexpr (GATED) v[1][i] *= ts1;
-        z[i] = __float_as_uint(v[0][i]);
-      }
-      if constexpr (!GATED) {
-        if (p.bias) act::add8(z, __ldg(reinterpret_cast<const uint4*>(p.bias + n)));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[0][i] = __uint_as_float(z[i]);
-      }
-      if (p.save0) put(p.save0, v[0]);
-      if constexpr (GATED) {
-        if (p.save1) put(p.save1, v[1]);
-      }
-      act::apply<8>(p.act, z);
-      if constexpr (!GATED) {
-        if (p.residual) act::add8(z, *reinterpret_cast<const uint4*>(p.residual + o));
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[0][i] = GATED ? __uint_as_float(z[i]) * v[GATED ? 1 : 0][i] : __uint_as_float(z[i]);
-      put(p.out, v[0]);
     }
-    if (p.S > 1) ptx::cluster_sync();        // the tile is reused only after every rank has read it
-    else __syncthreads();
+    if (tile_done || u + 1 == u1) {
+      // fp32 tile [batch row][weight row] (gated: 128 gate rows, then 128 up rows)
+      ptx::mbar_wait(tile_empty(nt & 1u), ((nt >> 1) & 1u) ^ 1u, p.status, abort_flag);
+      float* dst = tiles + (nt & 1u) * TILE + warp * 16 + g;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float* d = dst + size_t(8 * b + 2 * t) * ROWP;
+        d[0] = acc[b][0];
+        d[ROWP] = acc[b][1];
+        d[8] = acc[b][2];
+        d[ROWP + 8] = acc[b][3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(tile_full(nt & 1u));
+      ++nt;
+    }
+    if (tile_done) { ++tl; c = 0; }
+    else ++c;
   }
 }
 
@@ -357,10 +539,10 @@ struct NarrowDownParams {
 };
 
 template <int NB>
-__global__ void __launch_bounds__(narrow::kThreads)
+__global__ void __launch_bounds__(narrow::kDownWarps * 32)
 qlora_narrow_down_kernel(const __grid_constant__ NarrowDownParams p) {
   using namespace narrow;
-  __shared__ float part[kWarps][16][NB * 8 + 1];
+  __shared__ float part[kDownWarps][16][NB * 8 + 1];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -382,7 +564,7 @@ qlora_narrow_down_kernel(const __grid_constant__ NarrowDownParams p) {
   // pieces of 32 elements: lane t of a quad takes 8 of them; piece index strides over warps and ranks
   const int pieces = p.K / 32;
 #pragma unroll 4
-  for (int q = rank * kWarps + warp; q < pieces; q += p.S * kWarps) {
+  for (int q = rank * kDownWarps + warp; q < pieces; q += p.S * kDownWarps) {
     const size_t k = size_t(q) * 32 + t * 8;
     const uint4 a = __ldg(reinterpret_cast<const uint4*>(ar[0] + k)), c = __ldg(reinterpret_cast<const uint4*>(ar[1] + k));
 #pragma unroll
@@ -402,15 +584,15 @@ qlora_narrow_down_kernel(const __grid_constant__ NarrowDownParams p) {
   }
   __syncthreads();
   // the warps' sums into part[0], in warp order
-  for (int e = int(threadIdx.x); e < 16 * NB * 8; e += kThreads) {
+  for (int e = int(threadIdx.x); e < 16 * NB * 8; e += kDownWarps * 32) {
     float v = part[0][e / (NB * 8)][e % (NB * 8)];
-    for (int w = 1; w < kWarps; ++w) v += part[w][e / (NB * 8)][e % (NB * 8)];
+    for (int w = 1; w < kDownWarps; ++w) v += part[w][e / (NB * 8)][e % (NB * 8)];
     part[0][e / (NB * 8)][e % (NB * 8)] = v;
   }
   if (p.S > 1) ptx::cluster_sync();
   else __syncthreads();
   if (rank == 0) {
-    for (int e = int(threadIdx.x); e < 16 * p.M; e += kThreads) {
+    for (int e = int(threadIdx.x); e < 16 * p.M; e += kDownWarps * 32) {
       const int jj = e % 16, m = e / 16, j = grp * 16 + jj;
       if (j >= rows) continue;
       float v = 0.0f;
