@@ -258,6 +258,7 @@ qlora_status_t run_narrow(const qlora_weight_t* Wg, const qlora_weight_t* Wu, co
   const int cols = Wu ? narrow::kRows / 2 : narrow::kRows;
   p.tiles = int((N + cols - 1) / cols);
   p.chunks = int((K + narrow::CK - 1) / narrow::CK);
+  p.one = 1u;
   // Equal ranges of (tile, chunk) units over the SMs; without room for the partials, or with more
   // tiles than counters, whole tiles.
   p.status = ws_status(ws);

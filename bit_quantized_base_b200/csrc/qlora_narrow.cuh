@@ -34,8 +34,8 @@
 // 15 clusters of 8 or 33 of 4 fit beside each other on 148 SMs.)
 //
 // 20 warps, so that none waits for another's latency: 16 decode and multiply, each with its own ring
-// of code units (asynchronous copies, three units ahead, no barrier); 2 bring the chunks of X through a
-// ring that lets the decoding warps drift apart; 2 finish tiles (partials, arrival, epilogue) from one
+// of code units (asynchronous copies, three units ahead, no barrier); one brings the chunks of X (also
+// asynchronously) through a ring that lets the decoding warps drift apart; 3 finish tiles (partials, arrival, epilogue) from one
 // of two fp32 tile buffers while the others go on with the next tile.
 #pragma once
 #include <cuda_bf16.h>
@@ -48,8 +48,8 @@ namespace qlora {
 namespace narrow {
 constexpr int kMaxRows = 16;
 constexpr int kWarps = 16;                 // decoding warps
-constexpr int kXWarps = 2;                 // warps that bring X, taking turns
-constexpr int kEpiWarps = 2;               // warps that finish tiles
+constexpr int kXWarps = 1;                 // brings X
+constexpr int kEpiWarps = 3;               // finish tiles
 constexpr int kThreads = (kWarps + kXWarps + kEpiWarps) * 32;
 constexpr int CK = 256;                    // contraction elements of one chunk: 4 blocks of 64
 constexpr int NX = 4;                      // chunks of X in shared memory
@@ -62,6 +62,7 @@ constexpr int kMaxCounters = 1984;         // arrival counters in the workspace 
 // fp32 partials: at most two pieces of split tiles per CTA, [8 nb rows][kRows] each
 __host__ __device__ constexpr size_t partial_floats(int M) { return size_t(M) * kRows; }
 __host__ __device__ constexpr size_t x_bytes(int nb) { return size_t(nb) * 8 * CK * 2; }
+constexpr int kLoraDelay = 6;              // units (see lora_at)
 constexpr int kTableBytes = 256 * 128;     // 256 entries x 32 lanes x 4 bytes, or x 16 lanes x 8
 constexpr int kNfRegWords = 3;             // NF4: words of each 8 decoded from registers
 // decode table, codes ring, X ring, two fp32 tiles [8 nb][ROWP], barriers
@@ -77,54 +78,66 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Arrive on `bar` once this thread's asynchronous copies so far have landed (counted among the
+// arrivals the barrier was initialised with).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 // 16-byte asynchronous copy global -> shared; `bytes` 0 writes zeros instead.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// Entry e of the decode table, of which lane `l` reads its own copy.
+// Entries warp, warp + warps, ... of the decode table, every lane its own copy.
 template <int FMT>
-__device__ __forceinline__ void table_entry(uint32_t table, int e, int l) {
+__device__ __forceinline__ void fill_table(uint32_t table, int warp, int warps, int lane) {
   if constexpr (FMT == kFmtNF4 || FMT == kFmtNF4DQ) {
-    float lo = 0.0f, hi = 0.0f;
+    float mine = 0.0f;                        // the level of code lane % 16
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if ((e & 15) == i) lo = nf4_level_dev(i);
-      if ((e >> 4) == i) hi = nf4_level_dev(i);
+    for (int i = 0; i < 16; ++i)
+      if ((lane & 15) == i) mine = nf4_level_dev(i);
+    for (int e = warp; e < 256; e += warps) {
+      const float lo = __shfl_sync(0xFFFFFFFFu, mine, e & 15), hi = __shfl_sync(0xFFFFFFFFu, mine, e >> 4);
+      if (lane < 16)
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(table + uint32_t(e * 128 + lane * 8)), "f"(lo), "f"(hi) : "memory");
     }
-    if (l < 16)
-      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(table + uint32_t(e * 128 + l * 8)), "f"(lo), "f"(hi) : "memory");
   } else {
-    uint32_t o[4];
-    e2m1_decode8(uint32_t(e), o);             // codes 0 and 1 of the word
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(table + uint32_t(e * 128 + l * 4)), "r"(o[0]) : "memory");
+    for (int e = warp; e < 256; e += warps) {
+      uint32_t o[4];
+      e2m1_decode8(uint32_t(e), o);           // codes 0 and 1 of the word
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(table + uint32_t(e * 128 + lane * 4)), "r"(o[0]) : "memory");
+    }
   }
 }
-// The shared-memory address of byte b's entry: lane_base + 128 * byte.
-__device__ __forceinline__ uint32_t entry_addr(uint32_t lane_base, uint32_t w, int b) {
-  uint32_t a;
-  asm("mad.lo.u32 %0, %1, 128, %2;" : "=r"(a) : "r"(ptx::prmt(w, 0u, 0x4440u + uint32_t(b))), "r"(lane_base));
-  return a;
-}
+// Where this lane reads the decode table.  x128 is 128 in a form the compiler cannot see through (a
+// kernel argument times 128): the address of byte b's entry then is a multiply-add, on a pipe that the
+// decode leaves idle, and not a shift and add on the one that limits it.
+struct Table {
+  uint32_t base, x128;
+  __device__ __forceinline__ uint32_t addr(uint32_t w, int b) const {
+    return ptx::prmt(w, 0u, 0x4440u + uint32_t(b)) * x128 + base;
+  }
+};
 
 // One 64-element block's decoder: its scales, then 8 codes (a word) at a time into pairs 2 i, 2 i + 1.
 template <int FMT>
 struct BlockDecoder {                         // NF4, NF4DQ
   Lut16 t;
-  float absmax;
+  uint64_t absmax2;                           // the absmax twice
   __device__ __forceinline__ static uint32_t lane_base(uint32_t table, int lane) {
     return table + uint32_t(lane & 15) * 8u;
   }
   __device__ __forceinline__ void init(uint32_t raw) {
-    absmax = __uint_as_float(raw);
-    t = nf4_lut(absmax);
+    absmax2 = (uint64_t(raw) << 32) | raw;
+    t = nf4_lut(__uint_as_float(raw));
   }
-  __device__ __forceinline__ void word(int j, uint32_t w, uint32_t base, uint32_t (&o)[4]) const {
+  __device__ __forceinline__ void word(int j, uint32_t w, const Table& tab, uint32_t (&o)[4]) const {
     if (j >= kNfRegWords) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        float lo, hi;
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(lo), "=f"(hi) : "r"(entry_addr(base, w, b)));
-        o[b] = ptx::cvt_bf16x2(__fmul_rn(lo, absmax), __fmul_rn(hi, absmax));
+        uint64_t v;
+        asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(tab.addr(w, b)));
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(absmax2));
+        o[b] = ptx::cvt_bf16x2(__uint_as_float(uint32_t(v)), __uint_as_float(uint32_t(v >> 32)));
       }
     } else {
       // As lut16_lookup8, with the halves of the table chosen by a third permute whose selector is
@@ -170,11 +183,11 @@ struct E2m1Decoder {
       }
     }
   }
-  __device__ __forceinline__ void word(int j, uint32_t w, uint32_t base, uint32_t (&o)[4]) const {
+  __device__ __forceinline__ void word(int j, uint32_t w, const Table& tab, uint32_t (&o)[4]) const {
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       uint32_t v;
-      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(entry_addr(base, w, b)));
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(tab.addr(w, b)));
       o[b] = ptx::mul_bf16x2(v, s[j >> 1]);
     }
   }
@@ -202,6 +215,7 @@ struct NarrowParams {
   int* status;
   int M, N, K, r, ldzs;
   int tiles, chunks, iters, act;     // iters: units per CTA
+  uint32_t one;                      // 1 (see narrow::Table)
 };
 
 template <int FMT, bool GATED, int NB>
@@ -217,13 +231,14 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
   constexpr int TILE = NB * 8 * ROWP;                  // floats of one tile buffer
   float* tiles = reinterpret_cast<float*>(smem + kTableBytes + kWarps * NC * C_BYTES + NX * x_bytes(NB));
   uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + 2 * TILE);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * NX + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * NX + 5);
   volatile unsigned* s_last = reinterpret_cast<volatile unsigned*>(abort_flag + 1);
   const uint32_t b0 = ptx::smem_u32(bars);
   auto full = [&](uint32_t s) { return b0 + 8u * s; };
   auto empty = [&](uint32_t s) { return b0 + 8u * (NX + s); };
   auto tile_full = [&](uint32_t b) { return b0 + 8u * (2 * NX + b); };
   auto tile_empty = [&](uint32_t b) { return b0 + 8u * (2 * NX + 2 + b); };
+  const uint32_t table_full = b0 + 8u * (2 * NX + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int total = p.tiles * p.chunks;
@@ -231,47 +246,47 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
   const int blocks = p.K / 64;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NX; ++s) {
-      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(full(s), 32);            // every lane of the X warp, when its copies have landed
       ptx::mbar_init(empty(s), kWarps);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(tile_full(b), kWarps);
       ptx::mbar_init(tile_empty(b), kEpiWarps);
     }
+    ptx::mbar_init(table_full, kThreads / 32 - kWarps);
     *abort_flag = 0;
     ptx::fence_mbarrier_init();
   }
-  ptx::griddep_launch_dependents();
-  for (int e = warp; e < 256; e += kThreads / 32) table_entry<FMT>(table, e, lane);
   __syncthreads();
+  ptx::griddep_launch_dependents();
+  // the helper warps fill the decode table while the first codes are on their way
+  if (warp >= kWarps) {
+    fill_table<FMT>(table, warp - kWarps, kThreads / 32 - kWarps, lane);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(table_full);
+  }
 
   if (warp >= kWarps && warp < kWarps + kXWarps) {
     // ------------------------------------------------------------------ X
     // piece (b, i, lane) = 8 elements of batch row 8 b + lane / 4 at block 4 c + lane % 4, element 8 i
     // -- the order in which the products read them; zeros past M and K
-    for (int n = warp - kWarps; u0 + n < u1; n += kXWarps) {
-      const uint32_t s = uint32_t(n) % NX, ph = (uint32_t(n) / NX) & 1u;
-      const int blk = 4 * ((u0 + n) % p.chunks) + t;
-      uint4 v[NB][8];
+    uint32_t s = 0, ph = 0;
+    int c = u0 % p.chunks;
+    for (int u = u0; u < u1; ++u) {
+      if (!ptx::mbar_wait(empty(s), ph ^ 1u, p.status, abort_flag)) break;
+      const uint32_t at = xs + s * uint32_t(x_bytes(NB)) + uint32_t(lane) * 16u;
+      const int blk = 4 * c + t;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int row = 8 * b + g;
-        const bool ok = row < p.M && blk < blocks;
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + size_t(ok ? row : 0) * p.K + size_t(ok ? blk : 0) * 64);
+        const uint32_t bytes = row < p.M && blk < blocks ? 16u : 0u;
+        const __nv_bfloat16* src = bytes ? p.x + size_t(row) * p.K + size_t(blk) * 64 : p.x;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[b][i] = ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 8; ++i) cp_async_16(at + uint32_t(b * 8 + i) * 512u, src + (bytes ? i * 8 : 0), bytes);
       }
-      if (!ptx::mbar_wait(empty(s), ph ^ 1u, p.status, abort_flag)) break;
-      const uint32_t at = xs + s * uint32_t(x_bytes(NB)) + uint32_t(lane) * 16u;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 q = v[b][i];
-          ptx::st_shared_v4(at + uint32_t(b * 8 + i) * 512u, q.x, q.y, q.z, q.w);
-        }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(full(s));
+      cp_async_arrive(full(s));
+      if (++s == uint32_t(NX)) { s = 0; ph ^= 1u; }
+      if (++c == p.chunks) c = 0;
     }
     return;
   }
@@ -284,7 +299,7 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
     for (int u = u0; u < u1; ++nt) {
       const int tl = u / p.chunks;
       u = min((tl + 1) * p.chunks, u1);
-      ptx::mbar_wait_idle(tile_full(nt & 1u), (nt >> 1) & 1u, p.status, abort_flag);
+      ptx::mbar_wait(tile_full(nt & 1u), (nt >> 1) & 1u, p.status, abort_flag);
       const float* tile = tiles + (nt & 1u) * TILE;
       // the CTAs that share this tile
       const int first = (tl * p.chunks) / p.iters, last = (tl * p.chunks + p.chunks - 1) / p.iters;
@@ -296,16 +311,16 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
           const int m = e / (kRows / 4), q = e % (kRows / 4);
           __stcg(reinterpret_cast<float4*>(mine) + e, *reinterpret_cast<const float4*>(tile + size_t(m) * ROWP + 4 * q));
         }
-        __threadfence();
         ptx::named_bar_sync(1, kEpiWarps * 32);
         if (et == 0) {
+          __threadfence();                    // the piece (all threads' stores, ordered by the barrier)
           const unsigned n = atomicAdd(p.counters + tl, 1u);
           *s_last = n == unsigned(last - first) ? 1u : 0u;
           if (*s_last) p.counters[tl] = 0u;   // every piece has counted: back to zero for the next launch
+          __threadfence();
         }
         ptx::named_bar_sync(1, kEpiWarps * 32);
         finish = *s_last != 0u && *abort_flag == 0;
-        if (finish) __threadfence();
       }
       if (finish) {
         // 8 columns at a time: the pieces in order, then the epilogue
@@ -325,7 +340,7 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i) v[q][i] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
               for (int k = first; k <= last; ++k) {
                 const float* src = p.partial + (size_t(k) * 2 + ((k * p.iters) / p.chunks == tl ? 0 : 1)) * piece +
                                    size_t(m) * kRows + col;
@@ -375,7 +390,7 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
   }
 
   // ------------------------------------------------------------------ decode and multiply
-  const uint32_t lane_table = Dec::lane_base(table, lane);
+  const Table lane_table{Dec::lane_base(table, lane), p.one * 128u};
   // this warp's weight and its first row in the tile's columns
   const int wi = GATED && warp >= kWarps / 2 ? 1 : 0;
   const uint8_t* codes = p.w[wi].codes;
@@ -384,58 +399,124 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
   const __nv_bfloat16* lora_up = p.w[wi].lora_up;
   const int wrow = (GATED ? warp % (kWarps / 2) : warp) * 16;
   const uint32_t ring = cs + uint32_t(warp * NC * C_BYTES);
-  // Row j of the warp's group in tile tl, clamped to the weight (a clamped row's results are dropped).
+  // First row of the warp's group in tile tl, and row j of the group, clamped to the weight (a clamped
+  // row's results are dropped).
+  auto first_row = [&](int tl) { return min(tl * COLS + wrow, p.N - 1); };
   auto row_of = [&](int tl, int j) { return min(tl * COLS + wrow + j, p.N - 1); };
-  // A unit's codes: 16 rows x 128 bytes, 16-byte piece q of row j at q ^ (j & 1), so that the two
-  // halves of a block read by 8 neighbouring lanes fall into different banks.
-  auto copy_codes = [&](int tl, int c, uint32_t st) {
+  const uint32_t row_bytes = uint32_t(p.K) / 2;
+  // Codes: a cursor NC - 1 units ahead of the decode.  A unit is 16 rows x 128 bytes, 16-byte piece q
+  // of row j stored at q ^ (j & 1), so that the two halves of a block read by 8 neighbouring lanes
+  // fall into different banks; this lane copies piece lane % 8 of rows lane / 8 + 4 k.
+  const uint8_t* cptr = nullptr;              // this lane's piece of unit (ptl, pc) in row 0 of the group
+  uint32_t coff[4];                           // and how far its rows are from there
+  auto code_tile = [&](int tl, int c) {
+    const int r0 = first_row(tl);
+    cptr = codes + size_t(r0) * row_bytes + size_t(c) * (CK / 2) + (lane & 7) * 16;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = 4 * k + (lane >> 3), q = lane & 7;
-      const int blk = 4 * c + (q >> 1);
-      const bool ok = blk < blocks;
-      const uint8_t* src = codes + (size_t(row_of(tl, j)) * p.K) / 2 + (ok ? size_t(c) * (CK / 2) + q * 16 : 0);
-      cp_async_16(ring + st * uint32_t(C_BYTES) + uint32_t(j * 128 + ((q ^ (j & 1)) << 4)), src, ok ? 16u : 0u);
-    }
+    for (int k = 0; k < 4; ++k) coff[k] = uint32_t(row_of(tl, 4 * k + (lane >> 3)) - r0) * row_bytes;
   };
-  auto scale_of = [&](int tl, int c, uint32_t (&sc)[2]) {
-    const int blk = 4 * c + t;
+  int pleft = u1 - u0, pc = u0 % p.chunks, ptl = u0 / p.chunks;
+  uint32_t pst = 0;
+  if (pleft > 0) code_tile(ptl, pc);
+  const uint32_t cdst = ring + uint32_t((lane >> 3) * 128 + (((lane & 7) ^ ((lane >> 3) & 1)) << 4));
+  auto copy_next = [&]() {
+    if (pleft > 0) {
+      const uint32_t bytes = 4 * pc + ((lane & 7) >> 1) < blocks ? 16u : 0u;
+      const uint32_t dst = cdst + pst * uint32_t(C_BYTES);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sc[h] = 0u;
-      if (blk < blocks) {
-        const int n = row_of(tl, g + 8 * h);
-        if constexpr (FMT == kFmtNF4DQ) sc[h] = load_item_scale_dq(scales, scales2, 0, p.N, n, blk * 64, p.K).raw;
-        else sc[h] = load_item_scale<FMT>(scales, n, blk * 64, p.K).raw;
+      for (int k = 0; k < 4; ++k) cp_async_16(dst + uint32_t(k * 512), bytes ? cptr + coff[k] : codes, bytes);
+      cptr += CK / 2;
+      --pleft;
+      if (++pc == p.chunks) {
+        pc = 0;
+        if (pleft > 0) code_tile(++ptl, 0);
       }
     }
-  };
-  // cursor of the unit whose codes are copied next, NC - 1 units ahead
-  int ptl = u0 / p.chunks, pc = u0 % p.chunks, pu = u0;
-  auto copy_next = [&]() {
-    if (pu < u1) copy_codes(ptl, pc, uint32_t(pu - u0) % NC);
     ptx::cp_async_commit();
-    ++pu;
-    if (++pc == p.chunks) { pc = 0; ++ptl; }
+    pst = (pst + 1) % NC;
   };
+  // Block scales: a cursor one unit ahead.
   int tl = u0 / p.chunks, c = u0 % p.chunks;
-  uint32_t sc[2], nsc[2];
-  scale_of(tl, c, sc);
+  int stl = tl, sc_c = c;
+  const uint8_t* sptr[2];
+  constexpr int SB = FMT == kFmtMXFP4 ? 2 : 4;          // scale bytes of a block (NF4DQ: see below)
+  auto scale_tile = [&](int tl_, int c_) {
 #pragma unroll
-  for (int q = 0; q < NC - 1; ++q) copy_next();
+    for (int h = 0; h < 2; ++h)
+      sptr[h] = static_cast<const uint8_t*>(scales) + (size_t(row_of(tl_, g + 8 * h)) * blocks + 4 * c_ + t) * SB;
+  };
+  if constexpr (FMT != kFmtNF4DQ) scale_tile(stl, sc_c);
+  auto next_scales = [&](uint32_t (&out)[2]) {
+    const bool ok = 4 * sc_c + t < blocks;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      out[h] = 0u;
+      if (ok) {
+        if constexpr (FMT == kFmtNF4DQ)
+          out[h] = load_item_scale_dq(scales, scales2, 0, p.N, row_of(stl, g + 8 * h), (4 * sc_c + t) * 64, p.K).raw;
+        else if constexpr (FMT == kFmtMXFP4)
+          out[h] = __ldg(reinterpret_cast<const uint16_t*>(sptr[h]));
+        else
+          out[h] = __ldg(reinterpret_cast<const uint32_t*>(sptr[h]));
+      }
+      if constexpr (FMT != kFmtNF4DQ) sptr[h] += 4 * SB;
+    }
+    if (++sc_c == p.chunks) {
+      sc_c = 0;
+      ++stl;
+      if constexpr (FMT != kFmtNF4DQ) scale_tile(stl, 0);
+    }
+  };
+  uint32_t sc[2], nsc[2] = {0u, 0u};
+  copy_next();                                // the first unit's codes ahead of everything else
+  next_scales(sc);
+#pragma unroll
+  for (int q = 1; q < NC - 1; ++q) copy_next();
   float acc[NB][4];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
-  uint32_t xst = 0, xph = 0, nt = 0;
+  uint32_t xst = 0, xph = 0, nt = 0, cst = 0;
+  // The LoRA term of a tile belongs to the CTA with its chunk 0.  It needs Zs, which the kernel before
+  // (launched just ahead of this one) writes, so it is added after the CTA's first few units, or with
+  // its last unit of the tile: waiting earlier held CTAs back by 5 us.
+  auto lora_unit = [&](int u) { return max(u, min(u0 + kLoraDelay, min(u + p.chunks, u1) - 1)); };
+  int lora_at = c == 0 ? lora_unit(u0) : -1;
+  ptx::mbar_wait(table_full, 0, p.status, abort_flag);
   for (int u = u0; u < u1; ++u) {
     const bool tile_done = c + 1 == p.chunks;
+    if (c == 0) lora_at = lora_unit(u);
+    if (u == lora_at) {
+      // rows of B times Zs
+      ptx::griddep_wait();
+#pragma unroll
+      for (int k = 0; k < 64; k += 16)
+        if (k < p.r) {
+          const int ka = k + 2 * t, kb = ka + 8;
+          uint32_t a[2][2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const __nv_bfloat16* br = lora_up + size_t(row_of(tl, g + 8 * h)) * p.r;
+            a[h][0] = __ldg(reinterpret_cast<const uint32_t*>(br + ka));
+            a[h][1] = kb < p.r ? __ldg(reinterpret_cast<const uint32_t*>(br + kb)) : 0u;
+          }
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const int m = 8 * b + g;
+            const __nv_bfloat16* zr = p.zs + size_t(m) * p.ldzs + wi * p.r;
+            const uint32_t z0 = m < p.M ? __ldcg(reinterpret_cast<const uint32_t*>(zr + ka)) : 0u;
+            const uint32_t z1 = m < p.M && kb < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(zr + kb)) : 0u;
+            mma16816(acc[b], a[0][0], a[1][0], a[0][1], a[1][1], z0, z1);
+          }
+        }
+    }
     ptx::cp_async_wait<NC - 2>();
     __syncwarp();
     uint32_t w[2][8];
     {
-      const uint32_t at = ring + (uint32_t(u - u0) % NC) * uint32_t(C_BYTES);
+      const uint32_t at = ring + cst * uint32_t(C_BYTES);
+      cst = (cst + 1) % NC;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -445,32 +526,10 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
           w[h][4 * q] = v.x; w[h][4 * q + 1] = v.y; w[h][4 * q + 2] = v.z; w[h][4 * q + 3] = v.w;
         }
     }
-    // operands of the LoRA term, loaded a unit's work ahead (Zs is the kernel before's)
-    uint32_t la[4][2][2], lz[4][NB][2];
-    if (tile_done) {
-      ptx::griddep_wait();
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int ka = 16 * k + 2 * t, kb = ka + 8;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const __nv_bfloat16* br = lora_up + size_t(row_of(tl, g + 8 * h)) * p.r;
-          la[k][h][0] = ka < p.r ? __ldg(reinterpret_cast<const uint32_t*>(br + ka)) : 0u;
-          la[k][h][1] = kb < p.r ? __ldg(reinterpret_cast<const uint32_t*>(br + kb)) : 0u;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int m = 8 * b + g;
-          const __nv_bfloat16* zr = p.zs + size_t(m) * p.ldzs + wi * p.r;
-          lz[k][b][0] = m < p.M && ka < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(zr + ka)) : 0u;
-          lz[k][b][1] = m < p.M && kb < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(zr + kb)) : 0u;
-        }
-      }
-    }
     Dec dec[2];
     dec[0].init(sc[0]);
     dec[1].init(sc[1]);
-    if (u + 1 < u1) scale_of(tile_done ? tl + 1 : tl, tile_done ? 0 : c + 1, nsc);
+    if (u + 1 < u1) next_scales(nsc);
     // (the stage written here was read one unit ago, by products that have been issued since)
     copy_next();
     ptx::mbar_wait(full(xst), xph, p.status, abort_flag);   // giving up is seen at the tile's end
@@ -482,9 +541,7 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
       dec[1].word(i, w[1][i], lane_table, a[1]);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        // (lanes past the batch read nothing: fewer shared-memory cycles)
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (8 * b + g < p.M) x = ptx::ld_shared_v4(xb + uint32_t(b * 8 + i) * 512u);
+        const uint4 x = ptx::ld_shared_v4(xb + uint32_t(b * 8 + i) * 512u);
         mma16816(acc[b], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
         mma16816(acc[b], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
       }
@@ -494,16 +551,6 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
     if (++xst == uint32_t(NX)) { xst = 0; xph ^= 1u; }
     sc[0] = nsc[0];
     sc[1] = nsc[1];
-    if (tile_done) {
-      // the LoRA term: rows of B times Zs
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (16 * k < p.r) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            mma16816(acc[b], la[k][0][0], la[k][1][0], la[k][0][1], la[k][1][1], lz[k][b][0], lz[k][b][1]);
-        }
-    }
     if (tile_done || u + 1 == u1) {
       // fp32 tile [batch row][weight row] (gated: 128 gate rows, then 128 up rows)
       ptx::mbar_wait(tile_empty(nt & 1u), ((nt >> 1) & 1u) ^ 1u, p.status, abort_flag);
