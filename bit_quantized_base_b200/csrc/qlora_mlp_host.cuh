@@ -185,7 +185,7 @@ qlora_status_t launch_narrow_f(int fmt, const NarrowParams& p, unsigned grid, cu
 }
 
 NarrowWeight narrow_weight(const qlora_weight_t* W, const void* B) {
-  return NarrowWeight{W->codes, W->scales, W->fmt == QLORA_FMT_NF4_DQ ? W->scales2 : nullptr,
+  return NarrowWeight{W->scales, W->fmt == QLORA_FMT_NF4_DQ ? W->scales2 : nullptr,
                       W->fmt == QLORA_FMT_NVFP4 ? W->tensor_scale : nullptr,
                       static_cast<const __nv_bfloat16*>(B)};
 }
@@ -248,6 +248,10 @@ qlora_status_t run_narrow(const qlora_weight_t* Wg, const qlora_weight_t* Wu, co
   if (rc != QLORA_OK) return rc;
   p.w[0] = narrow_weight(Wg, Bg);
   if (Wu) p.w[1] = narrow_weight(Wu, Bu);
+  for (int i = 0; i < nw; ++i)
+    if (!tmap_2d(&p.tm_codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, (i ? Wu : Wg)->codes, uint64_t(K / 2), uint64_t(N),
+                 uint64_t(K / 2), narrow::CK / 2, narrow::kRows / nw, CU_TENSOR_MAP_SWIZZLE_128B))
+      return QLORA_ERR_CUDA;
   p.x = static_cast<const __nv_bfloat16*>(X);
   p.zs = static_cast<const __nv_bfloat16*>(Zs);
   p.M = int(M);

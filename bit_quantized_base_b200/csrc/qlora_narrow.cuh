@@ -33,9 +33,9 @@
 // (Splitting over clusters instead, with the sums in distributed shared memory, left SMs idle: only
 // 15 clusters of 8 or 33 of 4 fit beside each other on 148 SMs.)
 //
-// 20 warps, so that none waits for another's latency: 16 decode and multiply, each with its own ring
-// of code units (asynchronous copies, three units ahead, no barrier); one brings the chunks of X (also
-// asynchronously) through a ring that lets the decoding warps drift apart; 3 finish tiles (partials, arrival, epilogue) from one
+// 20 warps, so that none waits for another's latency: 16 decode and multiply; one brings each unit's
+// codes (one TMA box per weight: copies issued by the decoding warps stalled them whenever the memory
+// pushed back) and its chunk of X through a ring of 4 units; 3 finish tiles (partials, arrival, epilogue) from one
 // of two fp32 tile buffers while the others go on with the next tile.
 #pragma once
 #include <cuda_bf16.h>
@@ -52,9 +52,8 @@ constexpr int kXWarps = 1;                 // brings X
 constexpr int kEpiWarps = 3;               // finish tiles
 constexpr int kThreads = (kWarps + kXWarps + kEpiWarps) * 32;
 constexpr int CK = 256;                    // contraction elements of one chunk: 4 blocks of 64
-constexpr int NX = 4;                      // chunks of X in shared memory
-constexpr int NC = 4;                      // units of codes in shared memory, per warp
-constexpr int C_BYTES = 16 * CK / 2;       // one unit's codes of a warp: 16 rows x 128 bytes
+constexpr int NS = 4;                      // units in shared memory
+constexpr int C_BYTES = 256 * CK / 2;      // one unit's codes: 256 rows x 128 bytes, 128-byte swizzle
 constexpr int kRows = kWarps * 16;         // 256 weight rows per tile
 constexpr int ROWP = kRows + 4;            // pitch of the fp32 tile in shared memory (no conflicts)
 constexpr int kDownWarps = 8;              // warps of a down-projection CTA
@@ -65,9 +64,10 @@ __host__ __device__ constexpr size_t x_bytes(int nb) { return size_t(nb) * 8 * C
 constexpr int kLoraDelay = 6;              // units (see lora_at)
 constexpr int kTableBytes = 256 * 128;     // 256 entries x 32 lanes x 4 bytes, or x 16 lanes x 8
 constexpr int kNfRegWords = 3;             // NF4: words of each 8 decoded from registers
-// decode table, codes ring, X ring, two fp32 tiles [8 nb][ROWP], barriers
+__host__ __device__ constexpr size_t stage_bytes(int nb) { return C_BYTES + x_bytes(nb); }
+// unit ring (1024-byte aligned), decode table, two fp32 tiles [8 nb][ROWP], barriers
 __host__ __device__ constexpr size_t smem_bytes(int nb) {
-  return kTableBytes + size_t(kWarps) * NC * C_BYTES + NX * x_bytes(nb) + size_t(2) * nb * 8 * ROWP * 4 + 256;
+  return 1024 + NS * stage_bytes(nb) + kTableBytes + size_t(2) * nb * 8 * ROWP * 4 + 256;
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -199,13 +199,13 @@ struct BlockDecoder<kFmtNVFP4> : E2m1Decoder<kFmtNVFP4> {};
 }  // namespace narrow
 
 struct NarrowWeight {
-  const uint8_t* codes;              // [N, K/2]
   const void* scales;
   const float *scales2, *tensor_scale;
   const __nv_bfloat16* lora_up;      // B [N, r]
 };
 
 struct NarrowParams {
+  CUtensorMap tm_codes[2];           // codes [N, K/2] u8 of each weight, box {128, 256} (gated: {128, 128}), SW128
   NarrowWeight w[2];                 // gated: gate, up; else w[0]
   const __nv_bfloat16 *x, *zs;       // [M, K]; [M, ldzs], weight i at column i r
   const __nv_bfloat16 *bias, *residual;
@@ -224,57 +224,59 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
   using namespace narrow;
   using Dec = BlockDecoder<FMT>;
   constexpr int COLS = GATED ? kRows / 2 : kRows;      // output columns of a tile
-  extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t table = ptx::smem_u32(smem);
-  const uint32_t cs = table + uint32_t(kTableBytes);
-  const uint32_t xs = cs + uint32_t(kWarps * NC * C_BYTES);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr uint32_t STAGE = uint32_t(stage_bytes(NB));   // codes, then X
+  const uint32_t ring = ptx::smem_u32(smem);
+  const uint32_t table = ring + NS * STAGE;
   constexpr int TILE = NB * 8 * ROWP;                  // floats of one tile buffer
-  float* tiles = reinterpret_cast<float*>(smem + kTableBytes + kWarps * NC * C_BYTES + NX * x_bytes(NB));
+  float* tiles = reinterpret_cast<float*>(smem + NS * STAGE + kTableBytes);
   uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + 2 * TILE);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * NX + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * NS + 4);
   volatile unsigned* s_last = reinterpret_cast<volatile unsigned*>(abort_flag + 1);
   const uint32_t b0 = ptx::smem_u32(bars);
   auto full = [&](uint32_t s) { return b0 + 8u * s; };
-  auto empty = [&](uint32_t s) { return b0 + 8u * (NX + s); };
-  auto tile_full = [&](uint32_t b) { return b0 + 8u * (2 * NX + b); };
-  auto tile_empty = [&](uint32_t b) { return b0 + 8u * (2 * NX + 2 + b); };
-  const uint32_t table_full = b0 + 8u * (2 * NX + 4);
+  auto empty = [&](uint32_t s) { return b0 + 8u * (NS + s); };
+  auto tile_full = [&](uint32_t b) { return b0 + 8u * (2 * NS + b); };
+  auto tile_empty = [&](uint32_t b) { return b0 + 8u * (2 * NS + 2 + b); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int total = p.tiles * p.chunks;
   const int u0 = int(blockIdx.x) * p.iters, u1 = min(u0 + p.iters, total);
   const int blocks = p.K / 64;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NX; ++s) {
-      ptx::mbar_init(full(s), 32);            // every lane of the X warp, when its copies have landed
+    for (int s = 0; s < NS; ++s) {
+      ptx::mbar_init(full(s), 1 + 32);        // the codes' bytes; every lane's copies of X
       ptx::mbar_init(empty(s), kWarps);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(tile_full(b), kWarps);
       ptx::mbar_init(tile_empty(b), kEpiWarps);
     }
-    ptx::mbar_init(table_full, kThreads / 32 - kWarps);
     *abort_flag = 0;
     ptx::fence_mbarrier_init();
   }
   __syncthreads();
   ptx::griddep_launch_dependents();
-  // the helper warps fill the decode table while the first codes are on their way
-  if (warp >= kWarps) {
-    fill_table<FMT>(table, warp - kWarps, kThreads / 32 - kWarps, lane);
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(table_full);
-  }
 
   if (warp >= kWarps && warp < kWarps + kXWarps) {
-    // ------------------------------------------------------------------ X
+    // ------------------------------------------------------------------ codes and X
     // piece (b, i, lane) = 8 elements of batch row 8 b + lane / 4 at block 4 c + lane % 4, element 8 i
     // -- the order in which the products read them; zeros past M and K
     uint32_t s = 0, ph = 0;
-    int c = u0 % p.chunks;
+    int c = u0 % p.chunks, tl = u0 / p.chunks;
     for (int u = u0; u < u1; ++u) {
       if (!ptx::mbar_wait(empty(s), ph ^ 1u, p.status, abort_flag)) break;
-      const uint32_t at = xs + s * uint32_t(x_bytes(NB)) + uint32_t(lane) * 16u;
+      const uint32_t st = ring + s * STAGE;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(full(s), uint32_t(C_BYTES));
+        if (ptx::dcheck(ptx::tma_x_ok(c * (CK / 2), 1) && tl < p.tiles, p.status)) {
+          ptx::tma_load_2d(st, &p.tm_codes[0], full(s), c * (CK / 2), tl * COLS);
+          if constexpr (GATED) ptx::tma_load_2d(st + C_BYTES / 2, &p.tm_codes[1], full(s), c * (CK / 2), tl * COLS);
+        }
+      }
+      __syncwarp();
+      const uint32_t at = st + uint32_t(C_BYTES) + uint32_t(lane) * 16u;
       const int blk = 4 * c + t;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -285,15 +287,24 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
         for (int i = 0; i < 8; ++i) cp_async_16(at + uint32_t(b * 8 + i) * 512u, src + (bytes ? i * 8 : 0), bytes);
       }
       cp_async_arrive(full(s));
-      if (++s == uint32_t(NX)) { s = 0; ph ^= 1u; }
-      if (++c == p.chunks) c = 0;
+      if (++s == uint32_t(NS)) { s = 0; ph ^= 1u; }
+      if (++c == p.chunks) { c = 0; ++tl; }
     }
+    ptx::cp_async_wait<0>();
     return;
   }
 
   if (warp >= kWarps + kXWarps) {
     // ------------------------------------------------------------------ tiles
     const int et = int(threadIdx.x) - (kWarps + kXWarps) * 32;
+    // first, the adapter rows of the tiles whose LoRA term this CTA adds, into L2
+    for (int tl = (u0 + p.chunks - 1) / p.chunks; tl * p.chunks < u1; ++tl) {
+      const size_t row0 = size_t(tl) * COLS;
+      const size_t bytes = size_t(min(COLS, p.N - int(row0))) * size_t(p.r) * 2;
+      for (int i = 0; i < (GATED ? 2 : 1); ++i)
+        for (size_t o = size_t(et) * 128; o < bytes; o += kEpiWarps * 32 * 128)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.w[i].lora_up + row0 * p.r) + o));
+    }
     ptx::griddep_wait();
     uint32_t nt = 0;
     for (int u = u0; u < u1; ++nt) {
@@ -393,48 +404,14 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
   const Table lane_table{Dec::lane_base(table, lane), p.one * 128u};
   // this warp's weight and its first row in the tile's columns
   const int wi = GATED && warp >= kWarps / 2 ? 1 : 0;
-  const uint8_t* codes = p.w[wi].codes;
   const void* scales = p.w[wi].scales;
   const float* scales2 = p.w[wi].scales2;
   const __nv_bfloat16* lora_up = p.w[wi].lora_up;
   const int wrow = (GATED ? warp % (kWarps / 2) : warp) * 16;
-  const uint32_t ring = cs + uint32_t(warp * NC * C_BYTES);
-  // First row of the warp's group in tile tl, and row j of the group, clamped to the weight (a clamped
-  // row's results are dropped).
-  auto first_row = [&](int tl) { return min(tl * COLS + wrow, p.N - 1); };
+  // Row j of the warp's group in tile tl, clamped to the weight (a clamped row's results are dropped).
   auto row_of = [&](int tl, int j) { return min(tl * COLS + wrow + j, p.N - 1); };
-  const uint32_t row_bytes = uint32_t(p.K) / 2;
-  // Codes: a cursor NC - 1 units ahead of the decode.  A unit is 16 rows x 128 bytes, 16-byte piece q
-  // of row j stored at q ^ (j & 1), so that the two halves of a block read by 8 neighbouring lanes
-  // fall into different banks; this lane copies piece lane % 8 of rows lane / 8 + 4 k.
-  const uint8_t* cptr = nullptr;              // this lane's piece of unit (ptl, pc) in row 0 of the group
-  uint32_t coff[4];                           // and how far its rows are from there
-  auto code_tile = [&](int tl, int c) {
-    const int r0 = first_row(tl);
-    cptr = codes + size_t(r0) * row_bytes + size_t(c) * (CK / 2) + (lane & 7) * 16;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) coff[k] = uint32_t(row_of(tl, 4 * k + (lane >> 3)) - r0) * row_bytes;
-  };
-  int pleft = u1 - u0, pc = u0 % p.chunks, ptl = u0 / p.chunks;
-  uint32_t pst = 0;
-  if (pleft > 0) code_tile(ptl, pc);
-  const uint32_t cdst = ring + uint32_t((lane >> 3) * 128 + (((lane & 7) ^ ((lane >> 3) & 1)) << 4));
-  auto copy_next = [&]() {
-    if (pleft > 0) {
-      const uint32_t bytes = 4 * pc + ((lane & 7) >> 1) < blocks ? 16u : 0u;
-      const uint32_t dst = cdst + pst * uint32_t(C_BYTES);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) cp_async_16(dst + uint32_t(k * 512), bytes ? cptr + coff[k] : codes, bytes);
-      cptr += CK / 2;
-      --pleft;
-      if (++pc == p.chunks) {
-        pc = 0;
-        if (pleft > 0) code_tile(++ptl, 0);
-      }
-    }
-    ptx::cp_async_commit();
-    pst = (pst + 1) % NC;
-  };
+  // Code bytes of this lane's blocks: 16-byte piece q of row j of a unit is at q ^ (j % 8).
+  const uint32_t code_off = uint32_t(warp * 16 + g) * 128u;
   // Block scales: a cursor one unit ahead.
   int tl = u0 / p.chunks, c = u0 % p.chunks;
   int stl = tl, sc_c = c;
@@ -468,72 +445,69 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
     }
   };
   uint32_t sc[2], nsc[2] = {0u, 0u};
-  copy_next();                                // the first unit's codes ahead of everything else
   next_scales(sc);
-#pragma unroll
-  for (int q = 1; q < NC - 1; ++q) copy_next();
+  fill_table<FMT>(table, warp, kWarps, lane);   // while the first codes are on their way
   float acc[NB][4];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
-  uint32_t xst = 0, xph = 0, nt = 0, cst = 0;
+  uint32_t st = 0, ph = 0, nt = 0;
   // The LoRA term of a tile belongs to the CTA with its chunk 0.  It needs Zs, which the kernel before
   // (launched just ahead of this one) writes, so it is added after the CTA's first few units, or with
   // its last unit of the tile: waiting earlier held CTAs back by 5 us.
   auto lora_unit = [&](int u) { return max(u, min(u0 + kLoraDelay, min(u + p.chunks, u1) - 1)); };
   int lora_at = c == 0 ? lora_unit(u0) : -1;
-  ptx::mbar_wait(table_full, 0, p.status, abort_flag);
+  ptx::named_bar_sync(2, kWarps * 32);          // the decode table is complete
   for (int u = u0; u < u1; ++u) {
     const bool tile_done = c + 1 == p.chunks;
     if (c == 0) lora_at = lora_unit(u);
     if (u == lora_at) {
-      // rows of B times Zs
+      // rows of B times Zs: a lane takes the same r / 4 (r = 64: twice 8) rank elements of both, in the
+      // widest pieces they come in, all on their way before the first product
       ptx::griddep_wait();
+      uint4 la[2][2], lz[2][NB];
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      auto piece = [&](const __nv_bfloat16* row, int k) {
+        if (p.r >= 32) return k < p.r ? __ldcg(reinterpret_cast<const uint4*>(row + k + 8 * t)) : none;
+        if (k > 0) return none;
+        if (p.r == 16) {
+          const uint2 v = __ldcg(reinterpret_cast<const uint2*>(row + 4 * t));
+          return make_uint4(v.x, v.y, 0u, 0u);
+        }
+        return make_uint4(__ldcg(reinterpret_cast<const uint32_t*>(row + 2 * t)), 0u, 0u, 0u);
+      };
 #pragma unroll
-      for (int k = 0; k < 64; k += 16)
-        if (k < p.r) {
-          const int ka = k + 2 * t, kb = ka + 8;
-          uint32_t a[2][2];
+      for (int k = 0; k < 2; ++k) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const __nv_bfloat16* br = lora_up + size_t(row_of(tl, g + 8 * h)) * p.r;
-            a[h][0] = __ldg(reinterpret_cast<const uint32_t*>(br + ka));
-            a[h][1] = kb < p.r ? __ldg(reinterpret_cast<const uint32_t*>(br + kb)) : 0u;
-          }
+        for (int h = 0; h < 2; ++h) la[k][h] = piece(lora_up + size_t(row_of(tl, g + 8 * h)) * p.r, 32 * k);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const int m = 8 * b + g;
-            const __nv_bfloat16* zr = p.zs + size_t(m) * p.ldzs + wi * p.r;
-            const uint32_t z0 = m < p.M ? __ldcg(reinterpret_cast<const uint32_t*>(zr + ka)) : 0u;
-            const uint32_t z1 = m < p.M && kb < p.r ? __ldcg(reinterpret_cast<const uint32_t*>(zr + kb)) : 0u;
-            mma16816(acc[b], a[0][0], a[1][0], a[0][1], a[1][1], z0, z1);
-          }
+        for (int b = 0; b < NB; ++b)
+          lz[k][b] = 8 * b + g < p.M ? piece(p.zs + size_t(8 * b + g) * p.ldzs + wi * p.r, 32 * k) : none;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          mma16816(acc[b], la[k][0].x, la[k][1].x, la[k][0].y, la[k][1].y, lz[k][b].x, lz[k][b].y);
+          mma16816(acc[b], la[k][0].z, la[k][1].z, la[k][0].w, la[k][1].w, lz[k][b].z, lz[k][b].w);
         }
     }
-    ptx::cp_async_wait<NC - 2>();
-    __syncwarp();
+    ptx::mbar_wait(full(st), ph, p.status, abort_flag);     // giving up is seen at the tile's end
+    const uint32_t stage = ring + st * STAGE;
     uint32_t w[2][8];
-    {
-      const uint32_t at = ring + cst * uint32_t(C_BYTES);
-      cst = (cst + 1) % NC;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t j = uint32_t(g + 8 * h);
-          const uint4 v = ptx::ld_shared_v4(at + j * 128u + (((2u * t + q) ^ (j & 1u)) << 4));
-          w[h][4 * q] = v.x; w[h][4 * q + 1] = v.y; w[h][4 * q + 2] = v.z; w[h][4 * q + 3] = v.w;
-        }
-    }
+      for (int q = 0; q < 2; ++q) {
+        const uint4 v = ptx::ld_shared_v4(stage + code_off + uint32_t(h) * 1024u + ((uint32_t(2 * t + q) ^ uint32_t(g)) << 4));
+        w[h][4 * q] = v.x; w[h][4 * q + 1] = v.y; w[h][4 * q + 2] = v.z; w[h][4 * q + 3] = v.w;
+      }
     Dec dec[2];
     dec[0].init(sc[0]);
     dec[1].init(sc[1]);
     if (u + 1 < u1) next_scales(nsc);
-    // (the stage written here was read one unit ago, by products that have been issued since)
-    copy_next();
-    ptx::mbar_wait(full(xst), xph, p.status, abort_flag);   // giving up is seen at the tile's end
-    const uint32_t xb = xs + xst * uint32_t(x_bytes(NB)) + uint32_t(lane) * 16u;
+    const uint32_t xb = stage + uint32_t(C_BYTES) + uint32_t(lane) * 16u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t a[2][4];
@@ -547,8 +521,9 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
       }
     }
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(empty(xst));
-    if (++xst == uint32_t(NX)) { xst = 0; xph ^= 1u; }
+    // (every shared-memory read of the unit has returned: the products that took them have been issued)
+    if (lane == 0) ptx::mbar_arrive(empty(st));
+    if (++st == uint32_t(NS)) { st = 0; ph ^= 1u; }
     sc[0] = nsc[0];
     sc[1] = nsc[1];
     if (tile_done || u + 1 == u1) {
