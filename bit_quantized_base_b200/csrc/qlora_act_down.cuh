@@ -16,9 +16,11 @@
 // cluster (partial sums added in split order through distributed shared memory), and for a single
 // tile over C clusters (their sums added in cluster order by the last to arrive).
 //
-// Roles (320 threads): warps 0-7 load (one 64-column chunk ahead, in registers), differentiate,
-// write the gradients and the swizzled operand tiles, and at the end drain the accumulators;
-// warp 8 copies the chunk's rows of B (TMA); warp 9 allocates tensor memory and issues the MMAs.
+// Roles (576 threads): warps 0-15 load (one 64-column chunk ahead, in registers), differentiate,
+// write the gradients and the swizzled operand tiles, and at the end drain the accumulators (with 8
+// warps the arithmetic's latency, not the memory, set the pace: 295 against 91 us of traffic at 4096 x
+// 14336); warp 16 copies the chunk's rows of B (TMA); warp 17 allocates tensor memory and issues the
+// MMAs.
 #pragma once
 #include <cuda_bf16.h>
 #include "qlora_ptx.cuh"
@@ -30,12 +32,13 @@ namespace actdown {
 constexpr int BM = 128, BK = 64, NS = 2;
 constexpr int T_BYTES = BM * BK * 2;            // one operand tile: 16 KB
 constexpr int R_BYTES = 64 * 128;               // 64 rows of B, up to 64 wide
-constexpr int kWorkWarps = 8, kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 10 * 32;
+constexpr int kWorkWarps = 16, kTmaWarp = 16, kMmaWarp = 17;
+constexpr int kThreads = 18 * 32;
+constexpr int kRowStep = kWorkWarps * 4;        // rows between two vectors of a thread
 constexpr int kTmemCols = 128;                  // accumulator of stream b at column 64 b
 constexpr int kVec = BM * BK / 8 / (kWorkWarps * 32);   // 16-byte vectors a thread holds per tensor
 __host__ __device__ constexpr int stage_bytes(int nb) { return nb * (2 * T_BYTES + R_BYTES); }
-__host__ __device__ constexpr size_t smem_bytes(int nb) { return 1024 + size_t(NS) * stage_bytes(nb) + 4096; }
+__host__ __device__ constexpr size_t smem_bytes(int nb) { return 1024 + size_t(NS) * stage_bytes(nb) + 256 + kWorkWarps * 256; }
 
 // What rounding x0, x1 to the bf16 pair `hi` left out, as a bf16 pair (0 where that is not a number:
 // an infinite or NaN value is already in `hi`).
@@ -56,12 +59,12 @@ struct ActDownParams {
   int* status;
   float* cpart;                      // C > 1: [C][NB][128][rpad] fp32
   unsigned* ccount;                  // C > 1: [S] arrival counters, zero between launches
-  int M, N, r, rpad, ldzs, num_k, S, C, sps, act;
+  int M, N, r, rpad, ldzs, num_k, S, C, sps;
   float s;
   float zs_mul;                      // as DownParams
 };
 
-template <int NB>
+template <int NB, int ACT>
 __global__ void __launch_bounds__(actdown::kThreads, 1)
 qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
   using namespace actdown;
@@ -163,45 +166,30 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
     }
   } else {
     // ---------------------------------------------------------------- gradients and operand tiles
-    // Vector i of this thread: row vr + 32 i of the tile, columns 8 vc .. 8 vc + 7 of the chunk (a
+    // Vector i of this thread: row vr + kRowStep i of the tile, columns 8 vc .. 8 vc + 7 of the chunk (a
     // warp covers 4 rows of 128 contiguous bytes).
     const int vc = int(threadIdx.x) & 7, vr = int(threadIdx.x) >> 3;
     uint4 d[kVec], g[kVec], u[NB == 2 ? kVec : 1];
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    auto load = [&](int ks) {
+    auto load = [&](int ks, int i) {
       const int col = ks * BK + vc * 8;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const int row = m0 + vr + 32 * i;
-        const bool ok = row < p.M && col < p.N;
-        const size_t off = size_t(row) * p.N + col;
-        d[i] = ok ? ptx::ldg_stream_v4(p.dy + off) : zero;
-        g[i] = ok && p.a0 ? ptx::ldg_stream_v4(p.a0 + off) : zero;
-        if constexpr (NB == 2) u[i] = ok ? ptx::ldg_stream_v4(p.a1 + off) : zero;
-      }
+      const int row = m0 + vr + kRowStep * i;
+      const bool ok = row < p.M && col < p.N && ks < ks1;
+      const size_t off = size_t(row) * p.N + col;
+      d[i] = ok ? ptx::ldg_stream_v4(p.dy + off) : zero;
+      g[i] = ok && p.a0 ? ptx::ldg_stream_v4(p.a0 + off) : zero;
+      if constexpr (NB == 2) u[i] = ok ? ptx::ldg_stream_v4(p.a1 + off) : zero;
     };
-    auto pair_grad = [&](int act_id, float dd, float gg, float uu, float& o0, float& o1) {
+    auto pair_grad = [&](float dd, float gg, float uu, float& o0, float& o1) {
       float a, da;
-      switch (act_id) {
-        case act::kSilu: act::value_grad<act::kSilu>(gg, a, da); break;
-        case act::kGelu: act::value_grad<act::kGelu>(gg, a, da); break;
-        case act::kGeluTanh: act::value_grad<act::kGeluTanh>(gg, a, da); break;
-        default: act::value_grad<act::kNone>(gg, a, da); break;
-      }
+      act::value_grad<ACT>(gg, a, da);
       o0 = NB == 2 ? dd * uu * da : dd * da;
       o1 = dd * a;
     };
-    if (ks1 > ks0) load(ks0);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) load(ks0, i);
     for (int ks = ks0; ks < ks1; ++ks) {
       const uint32_t s = uint32_t(ks - ks0) % NS, ph = (uint32_t(ks - ks0) / NS) & 1u;
-      uint4 cd[kVec], cg_[kVec], cu[NB == 2 ? kVec : 1];
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        cd[i] = d[i];
-        cg_[i] = g[i];
-        if constexpr (NB == 2) cu[i] = u[i];
-      }
-      if (ks + 1 < ks1) load(ks + 1);
       // (a wait that gave up skips the shared-memory writes but not the barriers below, which all
       // work warps must reach)
       const bool stage_ok = ptx::mbar_wait(empty(s), ph ^ 1u, p.status, abort_flag);
@@ -210,17 +198,17 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
       for (int j = 0; j < 8; ++j) bsum[j] = 0.0f;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        const uint32_t wd[4] = {cd[i].x, cd[i].y, cd[i].z, cd[i].w};
-        const uint32_t wg[4] = {cg_[i].x, cg_[i].y, cg_[i].z, cg_[i].w};
+        const uint32_t wd[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
+        const uint32_t wg[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
         uint32_t wu[4] = {0u, 0u, 0u, 0u};
-        if constexpr (NB == 2) { wu[0] = cu[i].x; wu[1] = cu[i].y; wu[2] = cu[i].z; wu[3] = cu[i].w; }
+        if constexpr (NB == 2) { wu[0] = u[i].x; wu[1] = u[i].y; wu[2] = u[i].z; wu[3] = u[i].w; }
         uint32_t hi[NB][4], lo[NB][4], out1[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float x0, x1, y0, y1;
-          pair_grad(p.act, __uint_as_float(wd[j] << 16), __uint_as_float(wg[j] << 16),
+          pair_grad(__uint_as_float(wd[j] << 16), __uint_as_float(wg[j] << 16),
                     __uint_as_float(wu[j] << 16), x0, y0);
-          pair_grad(p.act, __uint_as_float(wd[j] & 0xFFFF0000u), __uint_as_float(wg[j] & 0xFFFF0000u),
+          pair_grad(__uint_as_float(wd[j] & 0xFFFF0000u), __uint_as_float(wg[j] & 0xFFFF0000u),
                     __uint_as_float(wu[j] & 0xFFFF0000u), x1, y1);
           if constexpr (NB == 1) { bsum[2 * j] += x0; bsum[2 * j + 1] += x1; }
           hi[0][j] = ptx::cvt_bf16x2(x0, x1);
@@ -231,7 +219,8 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
             out1[j] = p.ts1 ? ptx::cvt_bf16x2(y0 * up_ratio, y1 * up_ratio) : hi[1][j];
           }
         }
-        const int lr = vr + 32 * i, row = m0 + lr, col = ks * BK + vc * 8;
+        load(ks + 1, i);                         // the vector's place in the next chunk, as soon as it is free
+        const int lr = vr + kRowStep * i, row = m0 + lr, col = ks * BK + vc * 8;
         const uint32_t off = uint32_t(lr) * 128u + ((uint32_t(vc) ^ (uint32_t(lr) & 7u)) << 4);
 #pragma unroll
         for (int b = 0; b < NB && stage_ok; ++b) {

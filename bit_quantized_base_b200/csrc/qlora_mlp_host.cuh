@@ -78,12 +78,12 @@ qlora_status_t fill_fused(FusedExParams& p, const qlora_weight_t* W, bool dx, co
   return QLORA_OK;
 }
 
-template <int NB>
+template <int NB, int ACT>
 qlora_status_t launch_act_down_t(const ActDownParams& p, unsigned grid, unsigned cluster, cudaStream_t st) {
   const size_t smem = actdown::smem_bytes(NB);
-  if (!set_smem(qlora_act_down_kernel<NB>, smem)) return QLORA_ERR_CUDA;
+  if (!set_smem(qlora_act_down_kernel<NB, ACT>, smem)) return QLORA_ERR_CUDA;
   LaunchScope scope(kKindActDown, st);
-  if (launch_pdl_cluster(qlora_act_down_kernel<NB>, dim3(grid), dim3(actdown::kThreads), smem, st, p,
+  if (launch_pdl_cluster(qlora_act_down_kernel<NB, ACT>, dim3(grid), dim3(actdown::kThreads), smem, st, p,
                          cluster) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
@@ -125,12 +125,20 @@ qlora_status_t launch_act_down(int nb, int act, const void* dy, const void* a0, 
   p.S = dp.S;
   p.C = dp.C;
   p.sps = dp.sps;
-  p.act = act;
   p.s = s;
   p.zs_mul = zs_mul;
   const unsigned grid = unsigned(dp.tiles * dp.S * dp.C);
-  return nb == 2 ? launch_act_down_t<2>(p, grid, unsigned(dp.S), st)
-                 : launch_act_down_t<1>(p, grid, unsigned(dp.S), st);
+  const unsigned cl = unsigned(dp.S);
+  switch ((nb - 1) * act::kNumActs + act) {
+    case 0: return launch_act_down_t<1, act::kNone>(p, grid, cl, st);
+    case 1: return launch_act_down_t<1, act::kSilu>(p, grid, cl, st);
+    case 2: return launch_act_down_t<1, act::kGelu>(p, grid, cl, st);
+    case 3: return launch_act_down_t<1, act::kGeluTanh>(p, grid, cl, st);
+    case 4: return launch_act_down_t<2, act::kNone>(p, grid, cl, st);
+    case 5: return launch_act_down_t<2, act::kSilu>(p, grid, cl, st);
+    case 6: return launch_act_down_t<2, act::kGelu>(p, grid, cl, st);
+    default: return launch_act_down_t<2, act::kGeluTanh>(p, grid, cl, st);
+  }
 }
 
 // Runs `side_work` on the device's side stream beside `main_work` on `s`, joined into `s` again.
