@@ -146,9 +146,10 @@ bool set_smem(K kernel, size_t bytes) {
 
 // Launch with programmatic stream serialization: the kernel may begin while the previous kernel of
 // the stream runs; it waits for it (griddepcontrol.wait) after its own prologue.
+// early = false: an ordinary launch, which starts when the previous kernel has ended.
 template <typename P>
 cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                       const P& params) {
+                       const P& params, bool early = true) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -158,7 +159,7 @@ cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cu
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, params);
 }
 
@@ -391,14 +392,14 @@ enum Kind : int {
   kKindStreamFwd, kKindStreamDx, kKindStreamReduce, kKindShortFwd, kKindShortDx,
   kKindW4a8Quant, kKindW4a8Gemm, kKindNormFwd, kKindNormBwd, kKindNormDgamma,
   kKindGatedFwd, kKindGatedDx, kKindActFwd, kKindActDown, kKindBiasSum,
-  kKindNarrowDown, kNumKinds
+  kKindNarrowDown, kKindSplit, kNumKinds
 };
 const char* const kKindNames[kNumKinds] = {
     "fused_fwd", "fused_dx", "lora_down_T", "lora_down_U", "lora_wgrad",
     "grouped_fused_fwd", "grouped_fused_dx", "grouped_lora_down_T", "grouped_lora_down_U",
     "grouped_lora_wgrad", "stream_fwd", "stream_dx", "stream_reduce", "short_fwd", "short_dx",
     "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma",
-    "gated_fwd", "gated_dx", "act_fwd", "act_down", "bias_sum", "narrow_down_T"};
+    "gated_fwd", "gated_dx", "act_fwd", "act_down", "bias_sum", "narrow_down_T", "split_sum"};
 constexpr int kMaxProfiled = 65536;
 
 std::atomic<int64_t> g_launches{0};
@@ -516,10 +517,8 @@ qlora_status_t launch_fused_t(const FusedParams& p, int grid, bool grouped, cuda
 // W: one weight (E = 1) or E stacked weights; lora_up: B [E, N, r] (forward) or A [E, r, K] (dX).
 qlora_status_t launch_fused(const qlora_weight_t* W, bool dx, const void* act, const void* zs,
                             const void* lora_up, void* out, int64_t M, int r, int* status,
-                            const int32_t* offsets, int E, bool grouped, cudaStream_t st,
-                            bool act_late = false) {
+                            const int32_t* offsets, int E, bool grouped, cudaStream_t st) {
   FusedParams p{};
-  p.act_late = act_late ? 1 : 0;
   const int64_t N = W->N, K = W->K;
   const int64_t Kc = dx ? N : K;
   if (!tmap_2d(&p.tm_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, uint64_t(Kc), uint64_t(M),
@@ -579,12 +578,12 @@ qlora_status_t launch_fused(const qlora_weight_t* W, bool dx, const void* act, c
 }
 
 template <int FMT, bool DX, int MT>
-qlora_status_t launch_stream_t(const StreamParams& p, int grid, cudaStream_t st) {
+qlora_status_t launch_stream_t(const StreamParams& p, int grid, cudaStream_t st, bool early) {
   const size_t smem = stream::smem_bytes(p.xrows);
   if (!set_smem(qlora_stream_gemm_kernel<FMT, DX, MT>, smem)) return QLORA_ERR_CUDA;
   LaunchScope scope(DX ? kKindStreamDx : kKindStreamFwd, st);
   if (launch_pdl(qlora_stream_gemm_kernel<FMT, DX, MT>, dim3(grid), dim3(stream::kThreads), smem, st,
-                 p) != cudaSuccess)
+                 p, early) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
@@ -594,13 +593,12 @@ qlora_status_t launch_stream_t(const StreamParams& p, int grid, cudaStream_t st)
 qlora_status_t launch_stream(const qlora_weight_t* W, bool dx, const void* act, const void* zs,
                              const void* lora_up, void* out, int64_t M, int r, int* status,
                              float* partial, size_t partial_bytes, cudaStream_t st,
-                             bool act_late = false) {
+                             bool early = true) {
   const int64_t N = W->N, K = W->K;
   const int64_t Kc = dx ? N : K;
   const StreamPlan sp = stream_plan(N, K, M, dx, num_sms());
   if (sp.partial_bytes > partial_bytes) return QLORA_ERR_WORKSPACE;
   StreamParams p{};
-  p.act_late = act_late ? 1 : 0;
   p.xrows = int((M + 15) / 16 * 16);
   const int mt = p.xrows <= 128 ? 1 : 2;
   if (!tmap_2d(&p.tm_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, uint64_t(Kc), uint64_t(M),
@@ -630,18 +628,18 @@ qlora_status_t launch_stream(const qlora_weight_t* W, bool dx, const void* act, 
   p.segments = sp.segments;
   qlora_status_t rc;
   switch ((W->fmt * 2 + (dx ? 1 : 0)) * 2 + (mt - 1)) {
-    case 0: rc = launch_stream_t<kFmtNF4, false, 1>(p, sp.grid, st); break;
-    case 1: rc = launch_stream_t<kFmtNF4, false, 2>(p, sp.grid, st); break;
-    case 2: rc = launch_stream_t<kFmtNF4, true, 1>(p, sp.grid, st); break;
-    case 3: rc = launch_stream_t<kFmtNF4, true, 2>(p, sp.grid, st); break;
-    case 4: rc = launch_stream_t<kFmtMXFP4, false, 1>(p, sp.grid, st); break;
-    case 5: rc = launch_stream_t<kFmtMXFP4, false, 2>(p, sp.grid, st); break;
-    case 6: rc = launch_stream_t<kFmtMXFP4, true, 1>(p, sp.grid, st); break;
-    case 7: rc = launch_stream_t<kFmtMXFP4, true, 2>(p, sp.grid, st); break;
-    case 8: rc = launch_stream_t<kFmtNVFP4, false, 1>(p, sp.grid, st); break;
-    case 9: rc = launch_stream_t<kFmtNVFP4, false, 2>(p, sp.grid, st); break;
-    case 10: rc = launch_stream_t<kFmtNVFP4, true, 1>(p, sp.grid, st); break;
-    default: rc = launch_stream_t<kFmtNVFP4, true, 2>(p, sp.grid, st); break;
+    case 0: rc = launch_stream_t<kFmtNF4, false, 1>(p, sp.grid, st, early); break;
+    case 1: rc = launch_stream_t<kFmtNF4, false, 2>(p, sp.grid, st, early); break;
+    case 2: rc = launch_stream_t<kFmtNF4, true, 1>(p, sp.grid, st, early); break;
+    case 3: rc = launch_stream_t<kFmtNF4, true, 2>(p, sp.grid, st, early); break;
+    case 4: rc = launch_stream_t<kFmtMXFP4, false, 1>(p, sp.grid, st, early); break;
+    case 5: rc = launch_stream_t<kFmtMXFP4, false, 2>(p, sp.grid, st, early); break;
+    case 6: rc = launch_stream_t<kFmtMXFP4, true, 1>(p, sp.grid, st, early); break;
+    case 7: rc = launch_stream_t<kFmtMXFP4, true, 2>(p, sp.grid, st, early); break;
+    case 8: rc = launch_stream_t<kFmtNVFP4, false, 1>(p, sp.grid, st, early); break;
+    case 9: rc = launch_stream_t<kFmtNVFP4, false, 2>(p, sp.grid, st, early); break;
+    case 10: rc = launch_stream_t<kFmtNVFP4, true, 1>(p, sp.grid, st, early); break;
+    default: rc = launch_stream_t<kFmtNVFP4, true, 2>(p, sp.grid, st, early); break;
   }
   if (rc != QLORA_OK) return rc;
   StreamReduceParams rp{};
@@ -673,12 +671,12 @@ constexpr float kShortNvZsMul = 1.0f / 256.0f;
 float short_zs_mul(const qlora_weight_t* W) { return W->fmt == QLORA_FMT_NVFP4 ? kShortNvZsMul : 1.0f; }
 
 template <int FMT, bool DX>
-qlora_status_t launch_short_t(const ShortParams& p, int grid, cudaStream_t st) {
+qlora_status_t launch_short_t(const ShortParams& p, int grid, cudaStream_t st, bool early) {
   const size_t smem = DX ? shortk::dx_smem_bytes() : shortk::fwd_smem_bytes(p.xrows);
   auto kern = DX ? qlora_short_dx_kernel<FMT> : qlora_short_fwd_kernel<FMT>;
   if (!set_smem(kern, smem)) return QLORA_ERR_CUDA;
   LaunchScope scope(DX ? kKindShortDx : kKindShortFwd, st);
-  if (launch_pdl(kern, dim3(grid), dim3(shortk::kThreads), smem, st, p) != cudaSuccess)
+  if (launch_pdl(kern, dim3(grid), dim3(shortk::kThreads), smem, st, p, early) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
@@ -688,13 +686,12 @@ qlora_status_t launch_short_t(const ShortParams& p, int grid, cudaStream_t st) {
 qlora_status_t launch_short(const qlora_weight_t* W, bool dx, const void* act, const void* zs,
                             const void* lora_up, void* out, int64_t M, int r, void* ws,
                             float* partial, size_t partial_bytes, cudaStream_t st,
-                            bool act_late = false) {
+                            bool early = true) {
   const int64_t N = W->N, K = W->K;
   const int64_t Kc = dx ? N : K;
   const ShortPlan sp = short_plan(N, K, M, dx, num_sms());
   if (sp.partial_bytes > partial_bytes || sp.tiles > shortk::kMaxTiles) return QLORA_ERR_WORKSPACE;
   ShortParams p{};
-  p.act_late = act_late ? 1 : 0;
   p.xrows = int((M + 15) / 16 * 16);
   if (!tmap_2d(&p.tm_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, uint64_t(Kc), uint64_t(M),
                uint64_t(Kc) * 2, 64, uint32_t(p.xrows), CU_TENSOR_MAP_SWIZZLE_128B))
@@ -726,23 +723,32 @@ qlora_status_t launch_short(const qlora_weight_t* W, bool dx, const void* act, c
   p.one = 1u;
   p.zero = 0u;
   switch (W->fmt * 2 + (dx ? 1 : 0)) {
-    case 0: return launch_short_t<kFmtNF4, false>(p, sp.grid, st);
-    case 1: return launch_short_t<kFmtNF4, true>(p, sp.grid, st);
-    case 2: return launch_short_t<kFmtMXFP4, false>(p, sp.grid, st);
-    case 3: return launch_short_t<kFmtMXFP4, true>(p, sp.grid, st);
-    case 4: return launch_short_t<kFmtNVFP4, false>(p, sp.grid, st);
-    default: return launch_short_t<kFmtNVFP4, true>(p, sp.grid, st);
+    case 0: return launch_short_t<kFmtNF4, false>(p, sp.grid, st, early);
+    case 1: return launch_short_t<kFmtNF4, true>(p, sp.grid, st, early);
+    case 2: return launch_short_t<kFmtMXFP4, false>(p, sp.grid, st, early);
+    case 3: return launch_short_t<kFmtMXFP4, true>(p, sp.grid, st, early);
+    case 4: return launch_short_t<kFmtNVFP4, false>(p, sp.grid, st, early);
+    default: return launch_short_t<kFmtNVFP4, true>(p, sp.grid, st, early);
   }
 }
+
+// A second weight's adapter gradients in the same launch (the same X, N, K and r; one expert).
+// mul, div: dY is stored times mul / div.
+struct WgradSecond {
+  const void *dY, *T, *U;
+  void *dA, *dB;
+  const float *mul, *div;
+};
 
 // dB [E, N, r] = s dY_e^T T_e and dA [E, r, K] = s U_e^T X_e over each expert's rows.
 qlora_status_t launch_wgrad(const void* X, const void* dY, const void* T, const void* U, int64_t M,
                             int64_t N, int64_t K, int r, float s, void* dA, void* dB, void* ws,
                             const int32_t* offsets, int E, bool grouped, cudaStream_t st,
-                            const float* dy_mul = nullptr, const float* dy_div = nullptr) {
+                            const WgradSecond* second = nullptr) {
   WgradParams p{};
   const int rpad = rank_pad(r);
-  const WgradPlan wp = wgrad_plan(N, K, M, E, num_sms());
+  const int nw = second ? 2 : 1;
+  const WgradPlan wp = wgrad_plan(N, K, M, E * nw, num_sms());
   const CUtensorMapSwizzle rsw = swizzle_for_bytes(uint32_t(rpad) * 2);
   const uint64_t rows = uint64_t(M > 0 ? M : 1);
   if (!tmap_2d(&p.tm_l[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, uint64_t(N), rows,
@@ -754,8 +760,22 @@ qlora_status_t launch_wgrad(const void* X, const void* dY, const void* T, const 
       !tmap_2d(&p.tm_r[1], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, U, uint64_t(r), rows,
                uint64_t(r) * 2, uint32_t(rpad), 64, rsw))
     return QLORA_ERR_CUDA;
-  p.out0 = static_cast<__nv_bfloat16*>(dB);
-  p.out1 = static_cast<__nv_bfloat16*>(dA);
+  p.out[0] = static_cast<__nv_bfloat16*>(dB);
+  p.out[1] = static_cast<__nv_bfloat16*>(dA);
+  if (second) {
+    p.tm_l[3] = p.tm_l[1];
+    if (!tmap_2d(&p.tm_l[2], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, second->dY, uint64_t(N), rows,
+                 uint64_t(N) * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tmap_2d(&p.tm_r[2], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, second->T, uint64_t(r), rows,
+                 uint64_t(r) * 2, uint32_t(rpad), 64, rsw) ||
+        !tmap_2d(&p.tm_r[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, second->U, uint64_t(r), rows,
+                 uint64_t(r) * 2, uint32_t(rpad), 64, rsw))
+      return QLORA_ERR_CUDA;
+    p.out[2] = static_cast<__nv_bfloat16*>(second->dB);
+    p.out[3] = static_cast<__nv_bfloat16*>(second->dA);
+    p.l2_mul = second->mul;
+    p.l2_div = second->div;
+  }
   p.offsets = offsets;
   p.status = ws_status(ws);
   p.M = int(M);
@@ -768,11 +788,10 @@ qlora_status_t launch_wgrad(const void* X, const void* dY, const void* T, const 
   p.tiles1 = wp.tiles1;
   p.E = E;
   p.s = s;
-  p.l0_mul = dy_mul;
-  p.l0_div = dy_div;
+  p.nw = nw;
   const size_t smem = lora::smem_bytes(E);
   if (!set_smem(qlora_lora_wgrad_kernel, smem)) return QLORA_ERR_CUDA;
-  const unsigned grid = unsigned(int64_t(E) * (wp.tiles0 + wp.tiles1) * wp.S);
+  const unsigned grid = unsigned(int64_t(E) * nw * (wp.tiles0 + wp.tiles1) * wp.S);
   LaunchScope scope(grouped ? kKindGWgrad : kKindWgrad, st);
   if (launch_pdl_cluster(qlora_lora_wgrad_kernel, dim3(grid), dim3(lora::kThreads), smem, st, p,
                          unsigned(wp.S)) != cudaSuccess)

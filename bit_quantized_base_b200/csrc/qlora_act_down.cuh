@@ -12,15 +12,16 @@
 // rest of its binary32 value), two MMAs into one accumulator: U then carries no rounding of the
 // gradient, and dA = s U^T X, a product of U, only U's own.
 //
-// Work split as in lora_down: 128-row tiles, the N columns of a tile split over S CTAs of one
-// cluster (partial sums added in split order through distributed shared memory), and for a single
-// tile over C clusters (their sums added in cluster order by the last to arrive).
+// Work split: 128-row tiles; the N columns of a tile are split over S CTAs of one cluster (partial
+// sums added in split order through distributed shared memory) times C clusters, whose sums go to
+// the workspace and are added in cluster order by the last to arrive.  S C tiles fill the SMs twice:
+// two CTAs share an SM, so that one computes while the other waits for its loads or its MMAs (one CTA
+// per SM with two operand stages took 176 us where this one takes 110, at 4096 x 14336; 91 us of
+// traffic at the copy rate).
 //
-// Roles (576 threads): warps 0-15 load (one 64-column chunk ahead, in registers), differentiate,
-// write the gradients and the swizzled operand tiles, and at the end drain the accumulators (with 8
-// warps the arithmetic's latency, not the memory, set the pace: 295 against 91 us of traffic at 4096 x
-// 14336); warp 16 copies the chunk's rows of B (TMA); warp 17 allocates tensor memory and issues the
-// MMAs.
+// 256 threads: all load (one 64-column chunk ahead, in registers), differentiate, and write the
+// gradients and the swizzled operand tiles; one thread also copies the chunks' rows of B (TMA) and
+// issues the MMAs; at the end four warps drain the accumulators.
 #pragma once
 #include <cuda_bf16.h>
 #include "qlora_ptx.cuh"
@@ -29,22 +30,26 @@
 
 namespace qlora {
 namespace actdown {
-constexpr int BM = 128, BK = 64, NS = 2;
+constexpr int BM = 128, BK = 64;
 constexpr int T_BYTES = BM * BK * 2;            // one operand tile: 16 KB
 constexpr int R_BYTES = 64 * 128;               // 64 rows of B, up to 64 wide
-constexpr int kWorkWarps = 16, kTmaWarp = 16, kMmaWarp = 17;
-constexpr int kThreads = 18 * 32;
-constexpr int kRowStep = kWorkWarps * 4;        // rows between two vectors of a thread
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kRowStep = kWarps * 4;            // rows between two vectors of a thread
 constexpr int kTmemCols = 128;                  // accumulator of stream b at column 64 b
-constexpr int kVec = BM * BK / 8 / (kWorkWarps * 32);   // 16-byte vectors a thread holds per tensor
-__host__ __device__ constexpr int stage_bytes(int nb) { return nb * (2 * T_BYTES + R_BYTES); }
-__host__ __device__ constexpr size_t smem_bytes(int nb) { return 1024 + size_t(NS) * stage_bytes(nb) + 256 + kWorkWarps * 256; }
+constexpr int kVec = BM * BK / 8 / kThreads;    // 16-byte vectors a thread holds per tensor
+constexpr int kMaxTilesSplit = 240;             // counters: [tiles][S] of them when C > 1
+// operand tiles of one chunk, two chunks' rows of B, barriers, bias partials
+__host__ __device__ constexpr size_t smem_bytes(int nb) {
+  return 1024 + size_t(nb) * (2 * T_BYTES + 2 * R_BYTES) + 256 + kWarps * 256;
+}
 
-// What rounding x0, x1 to the bf16 pair `hi` left out, as a bf16 pair (0 where that is not a number:
-// an infinite or NaN value is already in `hi`).
+// What rounding x0, x1 to the bf16 pair `hi` left out, as a bf16 pair (0 where `hi` is infinite or NaN:
+// the value is all there).
 __device__ __forceinline__ uint32_t rest2(uint32_t hi, float x0, float x1) {
-  const float r0 = x0 - __uint_as_float(hi << 16), r1 = x1 - __uint_as_float(hi & 0xFFFF0000u);
-  return ptx::cvt_bf16x2(r0 - r0 == 0.0f ? r0 : 0.0f, r1 - r1 == 0.0f ? r1 : 0.0f);
+  const uint32_t lo = ptx::cvt_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xFFFF0000u));
+  const uint32_t top = ((hi & 0x7F807F80u) + 0x00800080u) & 0x80008000u;   // halves with a full exponent
+  if (top == 0u) return lo;
+  return lo & ~((top >> 15) * 0xFFFFu);
 }
 }  // namespace actdown
 
@@ -57,37 +62,33 @@ struct ActDownParams {
   const float *ts0, *ts1;            // NVFP4: tensor scales of the streams' weights, else null
   float* bias_part;                  // NB = 1: [tiles][N] partial column sums, or null
   int* status;
-  float* cpart;                      // C > 1: [C][NB][128][rpad] fp32
-  unsigned* ccount;                  // C > 1: [S] arrival counters, zero between launches
+  float* cpart;                      // C > 1: [tiles][C][NB][128][rpad] fp32
+  unsigned* ccount;                  // C > 1: [tiles][S] arrival counters, zero between launches
   int M, N, r, rpad, ldzs, num_k, S, C, sps;
   float s;
   float zs_mul;                      // as DownParams
 };
 
 template <int NB, int ACT>
-__global__ void __launch_bounds__(actdown::kThreads, 1)
+__global__ void __launch_bounds__(actdown::kThreads, 2)
 qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
   using namespace actdown;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  constexpr int STAGE = stage_bytes(NB);
-  uint8_t* tail = smem + size_t(NS) * STAGE;
+  uint8_t* tail = smem + size_t(NB) * (2 * T_BYTES + 2 * R_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(tail);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NS + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile unsigned* s_ticket = reinterpret_cast<volatile unsigned*>(tmem_slot + 2);
-  float* s_bias = reinterpret_cast<float*>(tail + 256);          // [kWorkWarps][64]
+  float* s_bias = reinterpret_cast<float*>(tail + 256);          // [kWarps][64]
   const uint32_t b0 = ptx::smem_u32(bars);
-  auto full = [&](uint32_t s) { return b0 + 8u * s; };
-  auto empty = [&](uint32_t s) { return b0 + 8u * (NS + s); };
-  const uint32_t acc_full = b0 + 8u * (2 * NS);
-  // stage s: per stream the rounded tile, the rest's tile; then the streams' B rows
-  auto tile = [&](uint32_t s, int b, int lo) {
-    return ptx::smem_u32(smem) + s * uint32_t(STAGE) + uint32_t(2 * b + lo) * T_BYTES;
-  };
-  auto rtile = [&](uint32_t s, int b) {
-    return ptx::smem_u32(smem) + s * uint32_t(STAGE) + uint32_t(2 * NB) * T_BYTES + uint32_t(b) * R_BYTES;
+  const uint32_t full = b0, empty = b0 + 8u, acc_full = b0 + 16u;    // operand tiles written / multiplied
+  auto b_full = [&](int q) { return b0 + 24u + 8u * uint32_t(q); };   // rows of B of an even / odd chunk
+  // stream b's rounded tile, the rest's tile; its rows of B
+  auto tile = [&](int b, int lo) { return ptx::smem_u32(smem) + uint32_t(2 * b + lo) * T_BYTES; };
+  auto rtile = [&](int q, int b) {
+    return ptx::smem_u32(smem) + uint32_t(2 * NB) * T_BYTES + uint32_t(q * NB + b) * R_BYTES;
   };
 
   const int per_tile = p.S * p.C;
@@ -97,15 +98,15 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
   const int ks0 = min(gs * p.sps, p.num_k), ks1 = min(ks0 + p.sps, p.num_k);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
-      ptx::mbar_init(full(s), 1 + kWorkWarps);     // the copy's expect-tx arrive + the work warps
-      ptx::mbar_init(empty(s), 1);
-    }
+    ptx::mbar_init(full, kWarps);
+    ptx::mbar_init(empty, 1);
     ptx::mbar_init(acc_full, 1);
+    ptx::mbar_init(b_full(0), 1);
+    ptx::mbar_init(b_full(1), 1);
     *abort_flag = 0;
     ptx::fence_mbarrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == 0) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -135,36 +136,15 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
     *reinterpret_cast<uint4*>(p.zs + size_t(rw) * p.ldzs + size_t(b) * p.r + c) = zs;
   };
 
-  if (warp == kTmaWarp) {
-    if (lane == 0) {
-      for (int ks = ks0; ks < ks1; ++ks) {
-        const uint32_t s = uint32_t(ks - ks0) % NS, ph = (uint32_t(ks - ks0) / NS) & 1u;
-        if (!ptx::mbar_wait_idle(empty(s), ph ^ 1u, p.status, abort_flag)) break;
-        ptx::mbar_arrive_expect_tx(full(s), uint32_t(NB) * r_bytes);
-        for (int b = 0; b < NB; ++b) ptx::tma_load_3d(rtile(s, b), &p.tm_r[b], full(s), 0, ks * BK, 0);
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0 && ks1 > ks0) {
-      const uint32_t idesc = ptx::idesc_bf16(128, uint32_t(p.rpad), 0u, 1u);
-      const uint32_t rsw = swz_mode_for_row_bytes(rowb);
-      bool ok = true;
-      for (int ks = ks0; ks < ks1; ++ks) {
-        const uint32_t s = uint32_t(ks - ks0) % NS, ph = (uint32_t(ks - ks0) / NS) & 1u;
-        if (!ptx::mbar_wait(full(s), ph, p.status, abort_flag)) { ok = false; break; }
-        ptx::tc_fence_after();
-        for (int b = 0; b < NB; ++b)
-          for (int lo = 0; lo < 2; ++lo)
-            for (int kk = 0; kk < BK / 16; ++kk) {
-              const uint64_t ad = ptx::smem_desc(tile(s, b, lo) + kk * 32, 16, 1024, ptx::kSw128);
-              const uint64_t bd = ptx::smem_desc(rtile(s, b) + kk * 16 * rowb, 64 * rowb, 8 * rowb, rsw);
-              ptx::mma_bf16(tmem + uint32_t(b) * 64u, ad, bd, idesc, (ks > ks0 || lo > 0 || kk > 0) ? 1u : 0u);
-            }
-        ptx::mma_commit(empty(s));
-      }
-      if (ok) ptx::mma_commit(acc_full);
-    }
-  } else {
+  auto copy_b = [&](int ks) {
+    const int q = (ks - ks0) & 1;
+    ptx::mbar_arrive_expect_tx(b_full(q), uint32_t(NB) * r_bytes);
+    for (int b = 0; b < NB; ++b) ptx::tma_load_3d(rtile(q, b), &p.tm_r[b], b_full(q), 0, ks * BK, 0);
+  };
+  const uint32_t idesc = ptx::idesc_bf16(128, uint32_t(p.rpad), 0u, 1u);
+  const uint32_t rsw = swz_mode_for_row_bytes(rowb);
+  if (threadIdx.x == 0 && ks1 > ks0) copy_b(ks0);
+  {
     // ---------------------------------------------------------------- gradients and operand tiles
     // Vector i of this thread: row vr + kRowStep i of the tile, columns 8 vc .. 8 vc + 7 of the chunk (a
     // warp covers 4 rows of 128 contiguous bytes).
@@ -189,10 +169,12 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) load(ks0, i);
     for (int ks = ks0; ks < ks1; ++ks) {
-      const uint32_t s = uint32_t(ks - ks0) % NS, ph = (uint32_t(ks - ks0) / NS) & 1u;
-      // (a wait that gave up skips the shared-memory writes but not the barriers below, which all
-      // work warps must reach)
-      const bool stage_ok = ptx::mbar_wait(empty(s), ph ^ 1u, p.status, abort_flag);
+      const uint32_t n = uint32_t(ks - ks0);
+      // the chunk before has been multiplied: its operand tiles and its rows of B are free  (a wait
+      // that gave up skips the shared-memory writes but not the barriers below, which all warps
+      // must reach)
+      const bool stage_ok = ptx::mbar_wait(empty, (n & 1u) ^ 1u, p.status, abort_flag);
+      if (threadIdx.x == 0 && stage_ok && ks + 1 < ks1) copy_b(ks + 1);
       float bsum[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) bsum[j] = 0.0f;
@@ -224,8 +206,8 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
         const uint32_t off = uint32_t(lr) * 128u + ((uint32_t(vc) ^ (uint32_t(lr) & 7u)) << 4);
 #pragma unroll
         for (int b = 0; b < NB && stage_ok; ++b) {
-          ptx::st_shared_v4(tile(s, b, 0) + off, hi[b][0], hi[b][1], hi[b][2], hi[b][3]);
-          ptx::st_shared_v4(tile(s, b, 1) + off, lo[b][0], lo[b][1], lo[b][2], lo[b][3]);
+          ptx::st_shared_v4(tile(b, 0) + off, hi[b][0], hi[b][1], hi[b][2], hi[b][3]);
+          ptx::st_shared_v4(tile(b, 1) + off, lo[b][0], lo[b][1], lo[b][2], lo[b][3]);
         }
         if (row < p.M && col < p.N) {
           const size_t o = size_t(row) * p.N + col;
@@ -237,7 +219,22 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0 && stage_ok) ptx::mbar_arrive(full(s));
+      if (lane == 0 && stage_ok) ptx::mbar_arrive(full);
+      if (threadIdx.x == 0 && stage_ok && ptx::mbar_wait(full, n & 1u, p.status, abort_flag) &&
+          ptx::mbar_wait(b_full(int(n & 1u)), (n >> 1) & 1u, p.status, abort_flag)) {
+        ptx::tc_fence_after();
+        for (int b = 0; b < NB; ++b)
+          for (int lo = 0; lo < 2; ++lo)
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              const uint64_t ad = ptx::smem_desc(tile(b, lo) + kk * 32, 16, 1024, ptx::kSw128);
+              const uint64_t bd =
+                  ptx::smem_desc(rtile(int(n & 1u), b) + kk * 16 * rowb, 64 * rowb, 8 * rowb, rsw);
+              ptx::mma_bf16(tmem + uint32_t(b) * 64u, ad, bd, idesc, (n > 0 || lo > 0 || kk > 0) ? 1u : 0u);
+            }
+        ptx::mma_commit(empty);
+        if (ks + 1 == ks1) ptx::mma_commit(acc_full);
+      }
+      __syncwarp();
       if constexpr (NB == 1) {
         if (p.bias_part) {
           // column sums of the tile: over the warp's 4 rows by shuffles, over the warps in order
@@ -246,15 +243,15 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
             bsum[j] += __shfl_xor_sync(0xFFFFFFFFu, bsum[j], 8);
             bsum[j] += __shfl_xor_sync(0xFFFFFFFFu, bsum[j], 16);
           }
-          ptx::named_bar_sync(1, kWorkWarps * 32);
+          ptx::named_bar_sync(1, kWarps * 32);
           if (lane < 8)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s_bias[warp * 64 + lane * 8 + j] = bsum[j];
-          ptx::named_bar_sync(1, kWorkWarps * 32);
+          ptx::named_bar_sync(1, kWarps * 32);
           if (threadIdx.x < 64) {
             const int col = ks * BK + int(threadIdx.x);
             float t = 0.0f;
-            for (int w = 0; w < kWorkWarps; ++w) t += s_bias[w * 64 + threadIdx.x];
+            for (int w = 0; w < kWarps; ++w) t += s_bias[w * 64 + threadIdx.x];
             if (col < p.N) p.bias_part[size_t(mt) * p.N + col] = t;
           }
         }
@@ -265,7 +262,7 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
   // ------------------------------------------------------------------ accumulators to U and Zs
   const bool have = ks1 > ks0;
   const int nrows = min(BM, p.M - m0);
-  const uint32_t part = ptx::smem_u32(smem);       // stage 0's tiles are free by then: stream b at
+  const uint32_t part = ptx::smem_u32(smem);       // the operand tiles are free by then: stream b at
   constexpr uint32_t PART = 32768u;                // b * PART
   if (warp < 4) {
     if (have) ptx::mbar_wait(acc_full, 0, p.status, abort_flag);
@@ -299,7 +296,7 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
     }
   }
   if (p.S > 1 || p.C > 1) {
-    float* const csum = p.cpart + size_t(cg) * NB * BM * p.rpad;
+    float* const csum = p.cpart + (size_t(mt) * p.C + cg) * NB * BM * p.rpad;
     ptx::cluster_sync();
     if (warp < 4 && *abort_flag == 0) {
 #pragma unroll 1
@@ -318,7 +315,7 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
     }
     ptx::cluster_sync();
     if (p.C > 1 && warp < 4) {
-      unsigned* const counter = p.ccount + split;
+      unsigned* const counter = p.ccount + mt * p.S + split;
       __threadfence();
       ptx::named_bar_sync(2, 128);
       if (threadIdx.x == 0) *s_ticket = atomicAdd(counter, 1u);
@@ -337,7 +334,7 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
           for (int k = 0; k < 8; ++k) v[k] = 0.0f;
           for (int k = 0; k < p.C; ++k) {
             const float4* src = reinterpret_cast<const float4*>(
-                p.cpart + ((size_t(k) * NB + b) * BM + lr) * p.rpad + c);
+                p.cpart + (((size_t(mt) * p.C + k) * NB + b) * BM + lr) * p.rpad + c);
             const float4 x = __ldcg(src), y = __ldcg(src + 1);
             v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
             v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
@@ -351,7 +348,7 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+  if (warp == 0) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
 // dbias[n] = the sum over the row tiles of their partial column sums, in tile order.

@@ -60,6 +60,9 @@
 //              Zs [M, 2r] holds both scaled Z, and the weight operand's other half is zero.
 //              NVFP4: the two tensor scales multiply their halves of the forward's accumulator;
 //              dX has one accumulator, so dU arrives multiplied by ts_up / ts_gate.
+//   Both (and kEpiAct's dX, which is the plain one otherwise) can split a tile's contraction over S
+//   work items, for batches whose tiles leave most CTA pairs idle: each item stores its fp32
+//   accumulator and qlora_split_kernel adds them in order and runs the epilogue.
 #pragma once
 #include <cuda_bf16.h>
 #include "qlora_ptx.cuh"
@@ -106,7 +109,6 @@ struct FusedParams {
   int num_n, num_k;                  // pair tiles over output columns; contraction steps
   int tail_split;                    // the last tail_split 512-row tiles run as 2 x 256-row tiles
   uint32_t zero;                     // 0 (see zero_after)
-  int act_late;                      // the activations come from the previous kernel: wait for it first
 };
 
 enum : int { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2 };
@@ -120,6 +122,8 @@ struct FusedExParams : FusedParams {
   const float* scales2_up;
   const float* tensor_scale_up;
   const __nv_bfloat16* lora_up_up;   // gated: Bu (forward), Au (dX)
+  int splits;                        // S: work items per tile
+  float* split_out;                  // S > 1: [S][M][output columns (gated forward: gate's, then up's)]
   const __nv_bfloat16 *bias, *residual;   // act: [N], [M, N], or null
   __nv_bfloat16 *save0, *save1;      // act: Z; gated: G and U; or null
   int act;                           // Act
@@ -258,11 +262,11 @@ struct ItemGeom {
   }
 };
 
-template <int FMT, bool DX, int EPI = kEpiPlain>
+template <int FMT, bool DX, int EPI = kEpiPlain, bool SPLIT = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fused::kThreads, 1)
 qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::type p) {
   using namespace fused;
-  static_assert(!(DX && EPI == kEpiAct), "the act epilogue is a forward one");
+  constexpr bool EX = EPI != kEpiPlain;
   constexpr bool GATED = EPI == kEpiGated;
   constexpr bool DUAL = GATED && DX;           // contraction over both weights' rows
   constexpr int TN = GATED && !DX ? HN : BN;   // output columns of a tile
@@ -343,20 +347,40 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
   const int nk1 = p.num_k;                                // contraction steps of one weight
   const int nk = DUAL ? 2 * nk1 : nk1;                    // of the tile, before its LoRA steps
   const int nt = GATED ? nk + (2 * p.r + BK - 1) / BK : nk + 1;   // all steps of the tile
+  // Work item t: a tile, or with S > 1 the t % S-th of S ranges [kb, ke) of tile t / S's steps.
+  int splits = 1;
+  if constexpr (SPLIT) splits = p.splits;
+  const int num_items = num_tiles * splits;
+  auto item_at = [&](int t, int& kb, int& ke) {
+    kb = 0;
+    ke = nt;
+    if constexpr (SPLIT) {
+      const int q = t % splits;
+      t /= splits;
+      kb = nt * q / splits;
+      ke = nt * (q + 1) / splits;
+    }
+    PairTile pt = pair_tile_at<DX>(grp_view, t, p.num_n, p.tail_split);
+    if constexpr (EX) {
+      if (pt.row0 + 2 * HM >= pt.row_end) pt.nb = 1;   // no rows in the second block
+    }
+    return pt;
+  };
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------------ activation producer
     if (lane == 0) {
       uint32_t i = 0;
       bool waited = false;
-      for (int t = pair; t < num_tiles; t += npairs) {
-        const PairTile pt = pair_tile_at<DX>(grp_view, t, p.num_n, p.tail_split);
+      for (int t = pair; t < num_items; t += npairs) {
+        int kb, ke;
+        const PairTile pt = item_at(t, kb, ke);
         const int m0 = pt.row0 + int(rank) * HM;      // this CTA's rows of block 0 (+256: block 1)
         bool ok = true;
-        for (int ks = 0; ks < nt; ++ks, ++i) {
+        for (int ks = kb; ks < ke; ++ks, ++i) {
           const uint32_t sx = i % NS, px = (i / NS) & 1u;
           if (!ptx::mbar_wait(empty_s(sx), px ^ 1u, p.status, abort_flag)) { ok = false; break; }
-          if ((ks == nk || p.act_late) && !waited) {
+          if (ks >= nk && !waited) {
             ptx::griddep_wait();
             waited = true;
           }
@@ -384,12 +408,13 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
     // ------------------------------------------------------------------ code producer
     if (lane == 0) {
       uint32_t j = 0;
-      for (int t = pair; t < num_tiles; t += npairs) {
-        const PairTile pt = pair_tile_at<DX>(grp_view, t, p.num_n, p.tail_split);
+      for (int t = pair; t < num_items; t += npairs) {
+        int kb, ke;
+        const PairTile pt = item_at(t, kb, ke);
         const int h0 = pt.nt * TN + (TN == BN ? int(rank) * HN : 0);   // this CTA's weight half
         const int wrow0 = pt.e * p.N;                 // the expert's first row of the codes
         bool ok = true;
-        for (int ks = 0; ks < nk; ++ks, ++j) {
+        for (int ks = kb; ks < min(ke, nk); ++ks, ++j) {
           const uint32_t sc = j % NC, pc = (j / NC) & 1u;
           if (!ptx::mbar_wait(empty_c(sc), pc ^ 1u, p.status, abort_flag)) { ok = false; break; }
           ptx::mbar_arrive_expect_tx(full_c(sc), C_BYTES);
@@ -425,18 +450,19 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
       constexpr uint64_t kAStage = (MB * X_BYTES) >> 4, kBStage = W_BYTES >> 4;
       constexpr uint64_t kABlk = X_BYTES >> 4, kAkk = 32 >> 4, kBkk = DX ? (2048 >> 4) : (32 >> 4);
       uint32_t i = 0, tc = 0;
-      for (int t = pair; t < num_tiles; t += npairs, ++tc) {
-        const int nb = pair_tile_at<DX>(grp_view, t, p.num_n, p.tail_split).nb;
+      for (int t = pair; t < num_items; t += npairs, ++tc) {
+        int kb, ke;
+        const int nb = item_at(t, kb, ke).nb;
         if (!ptx::mbar_wait_cluster(acc_empty, (tc & 1u) ^ 1u, p.status, abort_flag)) break;
         ptx::tc_fence_after();
         bool ok = true;
-        for (int ks = 0; ks < nt; ++ks, ++i) {
+        for (int ks = kb; ks < ke; ++ks, ++i) {
           const uint32_t st = i & (NS - 1);
           if (!ptx::mbar_wait_cluster(full_s(st), (i / NS) & 1u, p.status, abort_flag)) { ok = false; break; }
           ptx::tc_fence_after();
           const uint64_t a = a0 + st * kAStage, b = b0d + st * kBStage;
           if (ks < nk) {
-            const uint32_t acc0 = ks > 0 ? 1u : 0u;
+            const uint32_t acc0 = ks > kb ? 1u : 0u;
             if (nb == 2) {
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk) {
@@ -450,9 +476,10 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
             }
           } else {
             const int kks = GATED ? min(BK / 16, (2 * p.r - (ks - nk) * BK) / 16) : lora_kk;
+            const uint32_t acc0 = SPLIT && ks == kb ? 0u : 1u;     // a split range may hold LoRA steps only
             for (int kk = 0; kk < kks; ++kk) {
-              ptx::mma_bf16_pair(tmem, a + kk * kAkk, b + kk * kBkk, idesc, 1u);
-              if (nb == 2) ptx::mma_bf16_pair(tmem + BN, a + kABlk + kk * kAkk, b + kk * kBkk, idesc, 1u);
+              ptx::mma_bf16_pair(tmem, a + kk * kAkk, b + kk * kBkk, idesc, kk ? 1u : acc0);
+              if (nb == 2) ptx::mma_bf16_pair(tmem + BN, a + kABlk + kk * kAkk, b + kk * kBkk, idesc, kk ? 1u : acc0);
             }
           }
           ptx::mma_commit_pair(empty_s(st), 3);
@@ -464,9 +491,11 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
       // relay (other CTA): this CTA's weight half of step i is complete -> tell the leader
       const uint32_t full_leader0 = ptx::mapa(full_s(0), 0);
       uint32_t i = 0;
-      for (int t = pair; t < num_tiles; t += npairs) {
+      for (int t = pair; t < num_items; t += npairs) {
         bool ok = true;
-        for (int ks = 0; ks < nt; ++ks, ++i) {
+        int kb, ke;
+        item_at(t, kb, ke);
+        for (int ks = kb; ks < ke; ++ks, ++i) {
           const uint32_t st = i % NS;
           if (!ptx::mbar_wait(full_s(st), (i / NS) & 1u, p.status, abort_flag)) { ok = false; break; }
           ptx::mbar_arrive_remote(full_leader0 + 8u * st);
@@ -488,8 +517,9 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
     const uint32_t wsw = (uint32_t(lane) >> 1) & 3u;             // write swizzle of row `lane`
     const int rr0 = lane >> 2, rc = lane & 3;                     // read: row rr0 + 8 it, chunk rc
     uint32_t tc = 0;
-    for (int t = pair; t < num_tiles; t += npairs, ++tc) {
-      const PairTile pt = pair_tile_at<DX>(grp_view, t, p.num_n, p.tail_split);
+    for (int t = pair; t < num_items; t += npairs, ++tc) {
+      int kb, ke;
+      const PairTile pt = item_at(t, kb, ke);
       const int c0 = pt.nt * TN;
       const float ts = (FMT == kFmtNVFP4 && p.tensor_scale) ? __ldg(p.tensor_scale + pt.e) : 1.0f;
       float ts_up = 1.0f;
@@ -501,9 +531,9 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
         const int rbase = pt.row0 + blk * 2 * HM + int(rank) * HM + q * 32;
         if (rbase >= pt.row_end) continue;   // warp-uniform
         const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + uint32_t(blk * BN);
-        // One 32 x 32 block of this warp's rows (row = lane, `w` its 32 columns as bf16 pairs)
-        // through the staging tile to columns col0 .. col0+31 of `out`.
-        auto store_block = [&](const uint32_t (&w)[16], __nv_bfloat16* out, int col0) {
+        // 64 bytes of each of this warp's 32 rows (row = lane, `w` its 16 words) through the staging
+        // tile to byte `at` of the rows of `out`, which are `pitch` bytes long.
+        auto store_words = [&](const uint32_t (&w)[16], void* out, size_t pitch, size_t at, bool ok) {
 #pragma unroll
           for (int g = 0; g < 4; ++g)
             ptx::st_shared_v4(stg + uint32_t(lane) * 64u + ((uint32_t(g) ^ wsw) << 4), w[4 * g], w[4 * g + 1],
@@ -516,12 +546,31 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
             o[it] = ptx::ld_shared_v4(stg + rr * 64u + ((uint32_t(rc) ^ ((rr >> 1) & 3u)) << 4));
           }
           __syncwarp();
-          const int col = col0 + rc * 8;
 #pragma unroll
           for (int it = 0; it < 4; ++it) {
             const int row = rbase + it * 8 + rr0;
-            if (row < pt.row_end && col < ncols && ptx::dcheck(row >= 0 && pt.row_end <= p.M, p.status))
-              *reinterpret_cast<uint4*>(out + size_t(row) * ncols + col) = o[it];
+            if (row < pt.row_end && ok && ptx::dcheck(row >= 0 && pt.row_end <= p.M, p.status))
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + size_t(row) * pitch + at) = o[it];
+          }
+        };
+        // The same for 32 bf16 columns from col0.
+        auto store_block = [&](const uint32_t (&w)[16], __nv_bfloat16* out, int col0) {
+          const int col = col0 + rc * 8;
+          store_words(w, out, size_t(ncols) * 2, size_t(col) * 2, col < ncols);
+        };
+        // 32 binary32 columns from col0 of a split's accumulator.
+        [[maybe_unused]] auto store_split = [&](const uint32_t (&v)[32], int col0, int shift) {
+          if constexpr (SPLIT) {
+            const int width = GATED && !DX ? 2 * ncols : ncols;
+            float* out = p.split_out + size_t(t % splits) * size_t(p.M) * width;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = v[16 * h + j];
+              const int col = col0 + 16 * h + rc * 4;
+              store_words(w, out, size_t(width) * 4, size_t(shift + col) * 4, col < ncols);
+            }
           }
         };
 #pragma unroll 1
@@ -533,7 +582,9 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * ts);
           }
-          if constexpr (GATED && !DX) {
+          if constexpr (SPLIT && !(GATED && !DX)) {
+            store_split(v, c0 + cb * 32, 0);
+          } else if constexpr (GATED && !DX) {
             uint32_t u[32];
             ptx::tmem_ld_32x32b_x32(tb + uint32_t(HN + cb * 32), u);
             ptx::tmem_ld_wait(u);
@@ -541,22 +592,26 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
 #pragma unroll
               for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * ts_up);
             }
-            if (p.save0) {
+            if constexpr (SPLIT) {
+              store_split(v, c0 + cb * 32, 0);
+              store_split(u, c0 + cb * 32, ncols);
+            }
+            if (!SPLIT && p.save0) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) w[j] = ptx::cvt_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
               store_block(w, p.save0, c0 + cb * 32);
             }
-            if (p.save1) {
+            if (!SPLIT && p.save1) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) w[j] = ptx::cvt_bf16x2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
               store_block(w, p.save1, c0 + cb * 32);
             }
-            act::apply<32>(p.act, v);
+            if constexpr (!SPLIT) act::apply<32>(p.act, v);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               w[j] = ptx::cvt_bf16x2(__uint_as_float(v[2 * j]) * __uint_as_float(u[2 * j]),
                                      __uint_as_float(v[2 * j + 1]) * __uint_as_float(u[2 * j + 1]));
-          } else if constexpr (EPI == kEpiAct) {
+          } else if constexpr (EPI == kEpiAct && !DX) {
             const int row = rbase + lane, col = c0 + cb * 32;
             if (p.bias) {
 #pragma unroll
@@ -585,7 +640,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = ptx::cvt_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
           }
-          store_block(w, p.out, c0 + cb * 32);
+          if constexpr (!SPLIT) store_block(w, p.out, c0 + cb * 32);
         }
       }
       ptx::tc_fence_before();
@@ -601,29 +656,33 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
     // Cursor over this group's steps (every other step of the CTA's pipeline): tile t (the lt-th
     // of this pair), step ks of the tile (ks == nk is the LoRA step), weight-half origin h0.
     struct Cursor {
-      int t, lt, ks, h0, e;
+      int t, ks, kb, ke, h0, e;
+      uint32_t i, lora;              // pipeline step; LoRA steps of the items before this one
     };
-    auto set_tile = [&](Cursor& c) {
-      if (c.t < num_tiles) {
-        const PairTile pt = pair_tile_at<DX>(grp_view, c.t, p.num_n, p.tail_split);
+    auto set_item = [&](Cursor& c, int over) {
+      if (c.t < num_items) {
+        const PairTile pt = item_at(c.t, c.kb, c.ke);
+        c.ks = c.kb + over;
         c.h0 = pt.nt * TN + (TN == BN ? int(rank) * HN : 0);
         c.e = pt.e;
       }
     };
-    auto advance2 = [&](Cursor& c) {
-      c.ks += 2;
-      if (c.ks >= nt) {
-        c.ks -= nt;
+    auto advance = [&](Cursor& c, int by) {
+      c.i += uint32_t(by);
+      c.ks += by;
+      // (a split range may be one step long; any other item has two at least)
+      for (bool more = true; more && c.t < num_items && c.ks >= c.ke; more = SPLIT) {
+        const int over = c.ks - c.ke;
+        if (c.ke > nk) c.lora += uint32_t(c.ke - max(c.kb, nk));
         c.t += npairs;
-        ++c.lt;
-        set_tile(c);
+        set_item(c, over);
       }
     };
     // Step ks of a tile belongs to the up weight: dX, past the gate's rows; forward, in rank 1.
     auto is_up = [&](int ks) { return GATED && (DX ? ks >= nk1 : rank != 0); };
     auto scale_for = [&](const Cursor& c) {
       ItemScale sc{0u};
-      if (c.t < num_tiles && c.ks < nk) {
+      if (c.t < num_items && c.ks < nk) {
         const int kr = DUAL && c.ks >= nk1 ? c.ks - nk1 : c.ks;
         const int n = DX ? kr * BK + geo.row : c.h0 + geo.row;
         const int kcol = DX ? c.h0 + geo.chunk * 64 : kr * BK;
@@ -639,16 +698,17 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
       }
       return sc;
     };
-    Cursor cur{pair, 0, grp, 0, 0};
-    set_tile(cur);
+    Cursor cur{pair, 0, 0, 0, 0, 0, 0u, 0u};
+    set_item(cur, 0);
+    advance(cur, grp);
     Cursor pf = cur;
-    advance2(pf);
+    advance(pf, 2);
     ItemScale s_cur = scale_for(cur), s_next = scale_for(pf);
-    advance2(pf);
-    while (cur.t < num_tiles) {
+    advance(pf, 2);
+    while (cur.t < num_items) {
       const ItemScale s_pref = scale_for(pf);   // two own steps ahead
-      advance2(pf);
-      const uint32_t i = uint32_t(cur.lt * nt + cur.ks);           // pipeline step
+      advance(pf, 2);
+      const uint32_t i = cur.i;                                    // pipeline step
       const uint32_t sw = i % NS, pw = (i / NS) & 1u;
       const uint32_t rb = geo.op_row_base(ptx::smem_u32(wsm + sw * W_BYTES));
       if (cur.ks < nk) {
@@ -656,7 +716,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
         const int n = DX ? kr * BK + geo.row : cur.h0 + geo.row;
         const int kcol = DX ? cur.h0 + geo.chunk * 64 : kr * BK;
         const bool valid = n < p.N && kcol < p.K;
-        const uint32_t j = uint32_t(cur.lt * nk + cur.ks);          // code step
+        const uint32_t j = i - cur.lora;                             // code step
         const uint32_t scs = j % NC;
         if (!ptx::mbar_wait(full_c(scs), (j / NC) & 1u, p.status, abort_flag)) break;
         const uint32_t cb = ptx::smem_u32(cs + scs * C_BYTES);
@@ -724,7 +784,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
       if (lane == 0) ptx::mbar_arrive(full_s(sw));
       s_cur = s_next;
       s_next = s_pref;
-      advance2(cur);
+      advance(cur, 2);
     }
   }
 
@@ -733,6 +793,63 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
   ptx::cluster_sync();
   ptx::tc_fence_after();
   if (warp == kMmaWarp) ptx::tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// The end of a split contraction: adds the S accumulators of each output in order and runs the
+// epilogue that the fused kernel runs on one accumulator.  Memory bound: S binary32 matrices in.
+struct SplitParams {
+  const float* part;                 // [S][M][width]
+  const __nv_bfloat16 *bias, *residual;
+  __nv_bfloat16 *out, *save0, *save1;
+  long long groups;                  // M * n / 8
+  int S, n, width, gated, act;       // n: output columns; width: n, or 2 n (gated)
+};
+__global__ void __launch_bounds__(256) qlora_split_kernel(const __grid_constant__ SplitParams p) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const long long q = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (q >= p.groups) return;
+  const int per_row = p.n / 8;
+  const long long m = q / per_row;
+  const int col = int(q - m * per_row) * 8;
+  const size_t matrix = size_t(p.groups / per_row) * size_t(p.width);
+  auto sum8 = [&](int c, uint32_t (&z)[8]) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    const float* src = p.part + size_t(m) * p.width + c;
+#pragma unroll 4
+    for (int k = 0; k < p.S; ++k) {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(src + size_t(k) * matrix)),
+                   b = __ldcs(reinterpret_cast<const float4*>(src + size_t(k) * matrix) + 1);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = __float_as_uint(v[i]);
+  };
+  const size_t o = size_t(m) * p.n + col;
+  auto put = [&](__nv_bfloat16* dst, const uint32_t (&z)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = ptx::cvt_bf16x2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
+    *reinterpret_cast<uint4*>(dst + o) = make_uint4(w[0], w[1], w[2], w[3]);
+  };
+  uint32_t z[8], u[8];
+  sum8(col, z);
+  if (p.gated) {
+    sum8(p.n + col, u);
+    if (p.save1) put(p.save1, u);
+  }
+  if (p.bias) act::add8(z, __ldg(reinterpret_cast<const uint4*>(p.bias + col)));
+  if (p.save0) put(p.save0, z);
+  act::apply<8>(p.act, z);
+  if (p.gated) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = __float_as_uint(__uint_as_float(z[i]) * __uint_as_float(u[i]));
+  }
+  if (p.residual) act::add8(z, *reinterpret_cast<const uint4*>(p.residual + o));
+  put(p.out, z);
 }
 
 }  // namespace qlora

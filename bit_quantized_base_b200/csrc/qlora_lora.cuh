@@ -344,15 +344,16 @@ qlora_lora_down_kernel(const __grid_constant__ DownParams p) {
 }
 
 struct WgradParams {
-  CUtensorMap tm_l[2];  // L: dY [M, N] (problem 0, dB) / X [M, K] (problem 1, dA); box {64, 64} SW128
-  CUtensorMap tm_r[2];  // R: T [M, r] / U [M, r]; box {rpad, 64} SW(2 rpad)
-  __nv_bfloat16* out0;  // dB [E, N, r]: (p, j) at p * r + j
-  __nv_bfloat16* out1;  // dA [E, r, K]: (p, j) at j * K + p
+  // problems 0 and 1: dB and dA; 2 and 3 (nw = 2, one expert): the same of a second weight
+  CUtensorMap tm_l[4];  // L: dY [M, N] (problem 0, dB) / X [M, K] (problem 1, dA); box {64, 64} SW128
+  CUtensorMap tm_r[4];  // R: T [M, r] / U [M, r]; box {rpad, 64} SW(2 rpad)
+  __nv_bfloat16* out[4];  // dB [E, N, r]: (p, j) at p * r + j; dA [E, r, K]: (p, j) at j * K + p
   const int32_t* offsets;       // grouped: device [E+1]; nullptr: one expert of M rows
   int* status;
   int M, P0, P1, r, rpad, S, tiles0, tiles1, E;
   float s;
-  const float *l0_mul, *l0_div;  // not null: L of problem 0 holds dY * l0_mul / l0_div, taken out here
+  int nw;                        // weights
+  const float *l2_mul, *l2_div;  // not null: L of problem 2 holds dY * l2_mul / l2_div, taken out here
 };
 
 __global__ void __launch_bounds__(lora::kThreads, 1)
@@ -378,10 +379,12 @@ qlora_lora_wgrad_kernel(const __grid_constant__ WgradParams p) {
   const GroupView gv = build_group_view(p.offsets, p.E, p.M, 64, 1, s_off, s_first, p.status);
   const int tiles_pe = p.tiles0 + p.tiles1;
   const int tile = blockIdx.x / p.S, split = blockIdx.x % p.S;
-  const int e = tile / tiles_pe, et_tile = tile - e * tiles_pe;
-  const int prob = et_tile < p.tiles0 ? 0 : 1;
-  const int p0 = (et_tile - (prob ? p.tiles0 : 0)) * BM;
-  const int P = prob ? p.P1 : p.P0;
+  const int ew = tile / tiles_pe, et_tile = tile - ew * tiles_pe;
+  const int e = p.nw > 1 ? 0 : ew;                      // nw > 1: ew is the weight
+  const int side = et_tile < p.tiles0 ? 0 : 1;          // 0: dB, 1: dA
+  const int prob = p.nw > 1 ? 2 * ew + side : side;
+  const int p0 = (et_tile - (side ? p.tiles0 : 0)) * BM;
+  const int P = side ? p.P1 : p.P0;
   const bool table_ok = gv.total() > 0 || p.M == 0;
   const int row_begin = gv.off[e], row_end = gv.off[e + 1];
   const int chunks = table_ok ? (row_end - row_begin + 63) / 64 : 0;
@@ -410,23 +413,22 @@ qlora_lora_wgrad_kernel(const __grid_constant__ WgradParams p) {
   ptx::griddep_launch_dependents();
   const uint32_t rowb = uint32_t(p.rpad) * 2u;
   const uint32_t r_bytes = 64u * rowb;
-  __nv_bfloat16* out0 = p.out0 + size_t(e) * p.P0 * p.r;
-  __nv_bfloat16* out1 = p.out1 + size_t(e) * p.r * p.P1;
-  const float s_out = prob == 0 && p.l0_mul ? p.s * (__ldg(p.l0_div) / __ldg(p.l0_mul)) : p.s;
+  __nv_bfloat16* out = p.out[prob] + size_t(e) * p.r * P;
+  const float s_out = prob == 2 && p.l2_mul ? p.s * (__ldg(p.l2_div) / __ldg(p.l2_mul)) : p.s;
   // s * the reduction for columns c .. c+7 of output row pr (dB row-major, dA transposed)
   auto write8 = [&](int pr, int c, const float (&v)[8]) {
     if (c >= p.r) return;
-    if (!ptx::dcheck(pr >= 0 && pr < (prob == 0 ? p.P0 : p.P1) && e < p.E, p.status)) return;
-    if (prob == 0) {
+    if (!ptx::dcheck(pr >= 0 && pr < P && e < p.E, p.status)) return;
+    if (side == 0) {
       uint4 o;
       o.x = ptx::cvt_bf16x2(v[0] * s_out, v[1] * s_out);
       o.y = ptx::cvt_bf16x2(v[2] * s_out, v[3] * s_out);
       o.z = ptx::cvt_bf16x2(v[4] * s_out, v[5] * s_out);
       o.w = ptx::cvt_bf16x2(v[6] * s_out, v[7] * s_out);
-      *reinterpret_cast<uint4*>(out0 + size_t(pr) * p.r + c) = o;
+      *reinterpret_cast<uint4*>(out + size_t(pr) * p.r + c) = o;
     } else {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) out1[size_t(c + u) * p.P1 + pr] = __float2bfloat16_rn(v[u] * s_out);
+      for (int u = 0; u < 8; ++u) out[size_t(c + u) * P + pr] = __float2bfloat16_rn(v[u] * s_out);
     }
   };
 

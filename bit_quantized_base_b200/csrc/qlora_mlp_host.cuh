@@ -11,24 +11,32 @@ const float* ts_of(const qlora_weight_t* W) {
 
 bool act_valid(int act) { return act >= QLORA_ACT_NONE && act <= QLORA_ACT_GELU_TANH; }
 
-template <int FMT, bool DX, int EPI>
-qlora_status_t launch_fused_ex_t(const FusedExParams& p, int grid, cudaStream_t st) {
+template <int FMT, bool DX, int EPI, bool SPLIT>
+qlora_status_t launch_fused_ex_s(const FusedExParams& p, int grid, bool early, cudaStream_t st) {
   const size_t smem = fused::smem_bytes(1);
-  if (!set_smem(qlora_fused_gemm_kernel<FMT, DX, EPI>, smem)) return QLORA_ERR_CUDA;
-  LaunchScope scope(EPI == kEpiAct ? kKindActFwd : (DX ? kKindGatedDx : kKindGatedFwd), st);
-  if (launch_pdl(qlora_fused_gemm_kernel<FMT, DX, EPI>, dim3(grid), dim3(fused::kThreads), smem, st, p) !=
-      cudaSuccess)
+  if (!set_smem(qlora_fused_gemm_kernel<FMT, DX, EPI, SPLIT>, smem)) return QLORA_ERR_CUDA;
+  LaunchScope scope(EPI == kEpiAct ? (DX ? kKindFusedDx : kKindActFwd) : (DX ? kKindGatedDx : kKindGatedFwd), st);
+  if (launch_pdl(qlora_fused_gemm_kernel<FMT, DX, EPI, SPLIT>, dim3(grid), dim3(fused::kThreads), smem, st, p,
+                 early) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
+template <int FMT, bool DX, int EPI>
+qlora_status_t launch_fused_ex_t(const FusedExParams& p, int grid, bool early, cudaStream_t st) {
+  return p.splits > 1 ? launch_fused_ex_s<FMT, DX, EPI, true>(p, grid, early, st)
+                      : launch_fused_ex_s<FMT, DX, EPI, false>(p, grid, early, st);
+}
+
+// early: the launch may start beside the kernel before it (which must then not write this
+// one's activations).
 template <bool DX, int EPI>
-qlora_status_t launch_fused_ex(int fmt, const FusedExParams& p, int grid, cudaStream_t st) {
+qlora_status_t launch_fused_ex(int fmt, const FusedExParams& p, int grid, bool early, cudaStream_t st) {
   switch (fmt) {
-    case QLORA_FMT_NF4: return launch_fused_ex_t<kFmtNF4, DX, EPI>(p, grid, st);
-    case QLORA_FMT_MXFP4: return launch_fused_ex_t<kFmtMXFP4, DX, EPI>(p, grid, st);
-    case QLORA_FMT_NVFP4: return launch_fused_ex_t<kFmtNVFP4, DX, EPI>(p, grid, st);
-    default: return launch_fused_ex_t<kFmtNF4DQ, DX, EPI>(p, grid, st);
+    case QLORA_FMT_NF4: return launch_fused_ex_t<kFmtNF4, DX, EPI>(p, grid, early, st);
+    case QLORA_FMT_MXFP4: return launch_fused_ex_t<kFmtMXFP4, DX, EPI>(p, grid, early, st);
+    case QLORA_FMT_NVFP4: return launch_fused_ex_t<kFmtNVFP4, DX, EPI>(p, grid, early, st);
+    default: return launch_fused_ex_t<kFmtNF4DQ, DX, EPI>(p, grid, early, st);
   }
 }
 
@@ -44,7 +52,8 @@ bool tmap_codes(CUtensorMap* m, const qlora_weight_t* W, bool dx) {
 // [M, zr], `out`, and a grid of pair tiles of `tile_cols` output columns.
 qlora_status_t fill_fused(FusedExParams& p, const qlora_weight_t* W, bool dx, const void* act,
                           const void* zs, int zr, const void* lora_up, void* out, int64_t M, int r,
-                          int tile_cols, int* status, int& grid) {
+                          int tile_cols, int* status, const SplitPlan& split, float* split_out,
+                          int& grid) {
   const int64_t Kc = dx ? W->N : W->K;
   if (!tmap_2d(&p.tm_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act, uint64_t(Kc), uint64_t(M),
                uint64_t(Kc) * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -66,15 +75,42 @@ qlora_status_t fill_fused(FusedExParams& p, const qlora_weight_t* W, bool dx, co
   p.E = 1;
   p.num_n = int(((dx ? W->K : W->N) + tile_cols - 1) / tile_cols);
   p.num_k = int((Kc + fused::BK - 1) / fused::BK);
-  // as launch_fused: one CTA pair per two SMs, a short last wave in half tiles
-  int64_t tiles = (M + fused::BM - 1) / fused::BM * p.num_n;
+  // as launch_fused: one CTA pair per two SMs, a short last wave in half tiles (unless split)
+  int64_t tiles = row_tiles(M) * p.num_n;
   const int64_t most = num_sms() / 2;
-  int64_t pairs = tiles < most ? tiles : most;
-  const int64_t rem = tiles % pairs;
-  if (rem > 0 && 2 * rem <= pairs && tiles > pairs) p.tail_split = int(rem);
-  tiles += p.tail_split;
-  pairs = tiles < most ? tiles : most;
+  p.splits = split.S;
+  p.split_out = split_out;
+  if (split.S == 1) {
+    int64_t pairs = tiles < most ? tiles : most;
+    const int64_t rem = tiles % pairs;
+    if (rem > 0 && 2 * rem <= pairs && tiles > pairs) p.tail_split = int(rem);
+  }
+  const int64_t items = (tiles + p.tail_split) * split.S;
+  const int64_t pairs = items < most ? items : most;
   grid = int(2 * pairs);
+  return QLORA_OK;
+}
+
+// The sums and the epilogue of a split contraction whose accumulators `p` has written.
+qlora_status_t launch_split(const FusedExParams& p, int n, bool gated, cudaStream_t st) {
+  SplitParams q{};
+  q.part = p.split_out;
+  q.bias = p.bias;
+  q.residual = p.residual;
+  q.out = p.out;
+  q.save0 = p.save0;
+  q.save1 = p.save1;
+  q.groups = (long long)p.M * (n / 8);
+  q.S = p.splits;
+  q.n = n;
+  q.width = gated ? 2 * n : n;
+  q.gated = gated ? 1 : 0;
+  q.act = p.act;
+  if (!set_smem(qlora_split_kernel, 0)) return QLORA_ERR_CUDA;
+  LaunchScope scope(kKindSplit, st);
+  if (launch_pdl(qlora_split_kernel, dim3(unsigned((q.groups + 255) / 256)), dim3(256), 0, st, q) != cudaSuccess ||
+      cudaGetLastError() != cudaSuccess)
+    return QLORA_ERR_CUDA;
   return QLORA_OK;
 }
 
@@ -96,7 +132,7 @@ qlora_status_t launch_act_down(int nb, int act, const void* dy, const void* a0, 
                                float s, float zs_mul, void* sums, void* ws, cudaStream_t st) {
   ActDownParams p{};
   const int rpad = rank_pad(r);
-  const DownPlan dp = down_plan(M, N, 1, num_sms(), kDownWideCtas);
+  const ActDownPlan dp = act_down_plan(M, N, num_sms());
   for (int b = 0; b < nb; ++b) {
     if (!tmap_3d(&p.tm_r[b], B[b], uint64_t(r), uint64_t(N), 1, uint32_t(rpad), 64,
                  swizzle_for_bytes(uint32_t(rpad) * 2)))
@@ -114,7 +150,7 @@ qlora_status_t launch_act_down(int nb, int act, const void* dy, const void* a0, 
   p.status = ws_status(ws);
   if (dp.C > 1) {
     p.cpart = static_cast<float*>(sums);
-    p.ccount = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + kDownCountOffset);
+    p.ccount = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + kCounterOffset);
   }
   p.M = int(M);
   p.N = int(N);
@@ -141,7 +177,10 @@ qlora_status_t launch_act_down(int nb, int act, const void* dy, const void* a0, 
   }
 }
 
-// Runs `side_work` on the device's side stream beside `main_work` on `s`, joined into `s` again.
+// Runs `side_work` on the device's side stream beside `main_work` on `s`, joined into `s` again.  The
+// first kernel of main_work reads what act_down, the last kernel on `s`, writes, so it is launched
+// without the permission to start early; launched early, it would also hold back the fork event and
+// with it side_work, until its own end (measured).
 template <class F, class G>
 qlora_status_t fork_join(cudaStream_t s, F&& side_work, G&& main_work) {
   SideStream* side = side_stream();
@@ -153,9 +192,11 @@ qlora_status_t fork_join(cudaStream_t s, F&& side_work, G&& main_work) {
   if (cudaEventRecord(side->fork[slot], s) != cudaSuccess ||
       cudaStreamWaitEvent(side->stream, side->fork[slot], 0) != cudaSuccess)
     return QLORA_ERR_CUDA;
-  qlora_status_t st = side_work(side->stream);
+  // main_work first: its kernel takes the SMs it needs, side_work the ones it leaves idle
+  qlora_status_t st = main_work();
+  const qlora_status_t st2 = side_work(side->stream);
+  if (st == QLORA_OK) st = st2;
   if (cudaEventRecord(side->join[slot], side->stream) != cudaSuccess) return QLORA_ERR_CUDA;
-  if (st == QLORA_OK) st = main_work();
   if (cudaStreamWaitEvent(s, side->join[slot], 0) != cudaSuccess) return QLORA_ERR_CUDA;
   return st;
 }
@@ -199,7 +240,7 @@ NarrowWeight narrow_weight(const qlora_weight_t* W, const void* B) {
 }
 
 // Blocks of 8 batch rows, as the kernels are compiled for.
-int narrow_blocks(int64_t M) { return M <= 8 ? 1 : 2; }
+int narrow_blocks(int64_t M) { return M <= 8 ? 1 : (M <= 16 ? 2 : (M <= 32 ? 4 : 8)); }
 
 // T [nw][M, r] and Zs [M, nw r] of one or two adapters (Wu, Au null: one).
 qlora_status_t narrow_down(const qlora_weight_t* Wg, const qlora_weight_t* Wu, const void* X, const void* Ag,
@@ -223,7 +264,12 @@ qlora_status_t narrow_down(const qlora_weight_t* Wg, const qlora_weight_t* Wu, c
   d.s = scale;
   d.zs_mul = 1.0f;
   const unsigned groups = unsigned((nw * r + 15) / 16);
-  return nb == 1 ? launch_narrow_down_t<1>(d, groups, st) : launch_narrow_down_t<2>(d, groups, st);
+  switch (nb) {
+    case 1: return launch_narrow_down_t<1>(d, groups, st);
+    case 2: return launch_narrow_down_t<2>(d, groups, st);
+    case 4: return launch_narrow_down_t<4>(d, groups, st);
+    default: return launch_narrow_down_t<8>(d, groups, st);
+  }
 }
 
 // T and Zs by the kernels of the batch size: in the forward, and in a backward call that was not
@@ -231,7 +277,7 @@ qlora_status_t narrow_down(const qlora_weight_t* Wg, const qlora_weight_t* Wu, c
 qlora_status_t project_t(const qlora_weight_t* Wg, const qlora_weight_t* Wu, const void* X, const void* Ag,
                            const void* Au, uint8_t* T, uint8_t* Zs, int64_t M, int r, float scale, void* ws,
                            cudaStream_t s) {
-  if (M <= narrow::kMaxRows) return narrow_down(Wg, Wu, X, Ag, Au, T, Zs, M, r, scale, s);
+  if (M <= narrow::kMaxDownRows) return narrow_down(Wg, Wu, X, Ag, Au, T, Zs, M, r, scale, s);
   const int nw = Wu ? 2 : 1;
   for (int i = 0; i < nw; ++i) {
     const qlora_status_t st = launch_lora_down(
@@ -330,7 +376,9 @@ qlora_status_t qlora_gated_mlp_fwd(const qlora_weight_t* Wg, const qlora_weight_
   if (st != QLORA_OK) return st;
   FusedExParams p{};
   int grid = 0;
-  st = fill_fused(p, Wg, false, X, w + L.zs, 2 * r, Bg, H, M, r, fused::HN, ws_status(ws), grid);
+  const SplitPlan sp = split_fwd(Wg->N, Wg->K, M, r, 2, num_sms(), ws_bytes - L.partial);
+  st = fill_fused(p, Wg, false, X, w + L.zs, 2 * r, Bg, H, M, r, fused::HN, ws_status(ws), sp,
+                  reinterpret_cast<float*>(w + L.partial), grid);
   if (st != QLORA_OK) return st;
   if (!tmap_codes(&p.tm_codes_up, Wu, false)) return QLORA_ERR_CUDA;
   p.scales_up = Wu->scales;
@@ -340,7 +388,8 @@ qlora_status_t qlora_gated_mlp_fwd(const qlora_weight_t* Wg, const qlora_weight_
   p.save0 = static_cast<__nv_bfloat16*>(G);
   p.save1 = static_cast<__nv_bfloat16*>(U);
   p.act = act;
-  return launch_fused_ex<false, kEpiGated>(Wg->fmt, p, grid, s);
+  st = launch_fused_ex<false, kEpiGated>(Wg->fmt, p, grid, true, s);
+  return st != QLORA_OK || sp.S == 1 ? st : launch_split(p, p.N, true, s);
 }
 
 qlora_status_t qlora_gated_mlp_bwd(const qlora_weight_t* Wg, const qlora_weight_t* Wu, int act,
@@ -382,17 +431,16 @@ qlora_status_t qlora_gated_mlp_bwd(const qlora_weight_t* Wg, const qlora_weight_
                        w + L.sums, ws, s);
   if (st != QLORA_OK) return st;
   auto wgrads = [&](cudaStream_t q) {
-    qlora_status_t e = launch_wgrad(X, grad[0], Ts, z[0], M, N, K, r, scale, dAg, dBg, ws, nullptr, 1, false, q);
-    if (e != QLORA_OK) return e;
-    return launch_wgrad(X, grad[1], Ts + mr, z[1], M, N, K, r, scale, dAu, dBu, ws, nullptr, 1, false, q,
-                        ts[1], ts[1] ? ts[0] : nullptr);
+    const WgradSecond up{grad[1], Ts + mr, z[1], dAu, dBu, ts[1], ts[0]};
+    return launch_wgrad(X, grad[0], Ts, z[0], M, N, K, r, scale, dAg, dBg, ws, nullptr, 1, false, q, &up);
   };
   if (!dX) return wgrads(s);
   return fork_join(s, wgrads, [&]() {
     FusedExParams p{};
     int grid = 0;
+    const SplitPlan sp = split_dx(N, K, M, r, 2, num_sms(), ws_bytes - L.partial);
     qlora_status_t e = fill_fused(p, Wg, true, grad[0], w + L.zs, 2 * r, Ag, dX, M, r, fused::BN,
-                                  ws_status(ws), grid);
+                                  ws_status(ws), sp, reinterpret_cast<float*>(w + L.partial), grid);
     if (e != QLORA_OK) return e;
     if (!tmap_codes(&p.tm_codes_up, Wu, true) ||
         !tmap_2d(&p.tm_act_up, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, grad[1], uint64_t(N), uint64_t(M),
@@ -401,8 +449,8 @@ qlora_status_t qlora_gated_mlp_bwd(const qlora_weight_t* Wg, const qlora_weight_
     p.scales_up = Wu->scales;
     p.scales2_up = Wu->scales2;
     p.lora_up_up = static_cast<const __nv_bfloat16*>(Au);
-    p.act_late = 1;                          // dG and dU are the kernel before's
-    return launch_fused_ex<true, kEpiGated>(Wg->fmt, p, grid, s);
+    e = launch_fused_ex<true, kEpiGated>(Wg->fmt, p, grid, false, s);
+    return e != QLORA_OK || sp.S == 1 ? e : launch_split(p, p.K, false, s);
   });
 }
 
@@ -435,13 +483,16 @@ qlora_status_t qlora_linear_act_fwd(const qlora_weight_t* W, const void* X, cons
   if (st != QLORA_OK) return st;
   FusedExParams p{};
   int grid = 0;
-  st = fill_fused(p, W, false, X, w + L.zs, r, B, Y, M, r, fused::BN, ws_status(ws), grid);
+  const SplitPlan sp = split_fwd(W->N, W->K, M, r, 1, num_sms(), ws_bytes - L.partial);
+  st = fill_fused(p, W, false, X, w + L.zs, r, B, Y, M, r, fused::BN, ws_status(ws), sp,
+                  reinterpret_cast<float*>(w + L.partial), grid);
   if (st != QLORA_OK) return st;
   p.bias = static_cast<const __nv_bfloat16*>(bias);
   p.residual = static_cast<const __nv_bfloat16*>(residual);
   p.save0 = static_cast<__nv_bfloat16*>(Z_save);
   p.act = act;
-  return launch_fused_ex<false, kEpiAct>(W->fmt, p, grid, s);
+  st = launch_fused_ex<false, kEpiAct>(W->fmt, p, grid, true, s);
+  return st != QLORA_OK || sp.S == 1 ? st : launch_split(p, p.N, false, s);
 }
 
 qlora_status_t qlora_linear_act_bwd(const qlora_weight_t* W, const void* X, const void* A, const void* B,
@@ -499,11 +550,17 @@ qlora_status_t qlora_linear_act_bwd(const qlora_weight_t* W, const void* X, cons
   };
   if (!dX) return side_work(s);
   return fork_join(s, side_work, [&]() {
-    const bool late = grad[0] != nullptr;    // dZ is the kernel before's
-    if (short_dx) return launch_short(W, true, dZ, w + L.zs, A, dX, M, r, ws, part, region, s, late);
+    const bool early = grad[0] == nullptr;   // else dZ is act_down's
+    if (short_dx) return launch_short(W, true, dZ, w + L.zs, A, dX, M, r, ws, part, region, s, early);
     if (stream_dx)
-      return launch_stream(W, true, dZ, w + L.zs, A, dX, M, r, ws_status(ws), part, region, s, late);
-    return launch_fused(W, true, dZ, w + L.zs, A, dX, M, r, ws_status(ws), nullptr, 1, false, s, late);
+      return launch_stream(W, true, dZ, w + L.zs, A, dX, M, r, ws_status(ws), part, region, s, early);
+    FusedExParams p{};
+    int grid = 0;
+    const SplitPlan sp = split_dx(N, K, M, r, 1, num_sms(), region);
+    qlora_status_t e = fill_fused(p, W, true, dZ, w + L.zs, r, A, dX, M, r, fused::BN, ws_status(ws), sp, part, grid);
+    if (e != QLORA_OK) return e;
+    e = launch_fused_ex<true, kEpiAct>(W->fmt, p, grid, early, s);
+    return e != QLORA_OK || sp.S == 1 ? e : launch_split(p, p.K, false, s);
   });
 }
 

@@ -5,6 +5,64 @@
 namespace qlora {
 namespace {
 
+// Work items a pair tile's contraction is split into (1: not).  A pair takes about 0.55 us for a step
+// of a 512-row tile and 0.33 us for one of at most 256 rows (measured); a split costs its fp32
+// accumulators, written and read once, and a launch.  `room`: bytes for the accumulators.
+struct SplitPlan {
+  int S;
+  size_t bytes;
+};
+SplitPlan split_plan(int64_t M, int64_t tiles, int64_t steps, int64_t width, int sms, size_t room) {
+  SplitPlan best{1, 0};
+  if (M <= 0) return best;
+  const int64_t pairs = sms / 2;
+  const double step_us = M > 256 ? 0.55 : 0.33;
+  double cost = double((tiles + pairs - 1) / pairs) * double(steps) * step_us;
+  for (int S = 2; S <= 16 && steps / S >= 4; ++S) {
+    const size_t bytes = size_t(S) * size_t(M) * size_t(width) * 4;
+    if (bytes > room) break;
+    const double c = double((tiles * S + pairs - 1) / pairs) * double((steps + S - 1) / S) * step_us + 5.0 +
+                     double(bytes) * 2 / 4.0e6;
+    if (c < 0.95 * cost) {
+      cost = c;
+      best = SplitPlan{S, bytes};
+    }
+  }
+  return best;
+}
+int64_t row_tiles(int64_t M) { return (M + fused::BM - 1) / fused::BM; }
+// The fused kernel's tiles and steps: forward of n weights, dX of n weights.
+SplitPlan split_fwd(int64_t N, int64_t K, int64_t M, int r, int n, int sms, size_t room) {
+  const int64_t cols = n == 2 ? fused::HN : fused::BN;
+  return split_plan(M, row_tiles(M) * ((N + cols - 1) / cols), (K + 63) / 64 + (n * r + 63) / 64, n * N, sms, room);
+}
+SplitPlan split_dx(int64_t N, int64_t K, int64_t M, int r, int n, int sms, size_t room) {
+  return split_plan(M, row_tiles(M) * ((K + fused::BN - 1) / fused::BN), n * ((N + 63) / 64) + (n * r + 63) / 64, K,
+                    sms, room);
+}
+
+// The plan of the act_down kernel: S CTAs a cluster, C clusters a tile, two CTAs per SM, at least two
+// 64-column chunks each.
+struct ActDownPlan {
+  int tiles, S, C, sps, num_k;
+};
+ActDownPlan act_down_plan(int64_t M, int64_t N, int sms) {
+  ActDownPlan p{};
+  p.tiles = int((M + 127) / 128);
+  p.num_k = int((N + 63) / 64);
+  int per = p.tiles > 0 ? 2 * sms / p.tiles : 1;               // CTAs a tile may have
+  per = std::max(1, std::min(per, p.num_k / 2));
+  p.S = std::min(per, kMaxClusterSplits);
+  p.C = p.S == kMaxClusterSplits && p.tiles <= actdown::kMaxTilesSplit ? per / p.S : 1;
+  p.sps = (p.num_k + p.S * p.C - 1) / (p.S * p.C);
+  return p;
+}
+
+// Bytes of its cluster sums: C > 1 only with full clusters, so tiles * C <= 2 SMs / 8 whatever M.
+size_t act_down_sum_bytes(int nb, int r, int sms) {
+  return size_t(2 * sms / kMaxClusterSplits) * nb * 128 * size_t(rank_pad(r)) * 4;
+}
+
 // n = 2 (gated) or 1 weights.  header | Zs [M, n r] | T [n][M, r] | backward: U [n][M, r],
 // gradients of the pre-activations [n][M, N] bf16, the projection's cluster sums, bias partials
 // [ceil(M/128)][N] fp32 (n = 1), and the short-batch kernels' fp32 partials.
@@ -31,13 +89,17 @@ MlpLayout mlp_layout(int64_t N, int64_t K, int64_t M, int r, int n, bool bwd, in
   if (bwd) {
     L.u = take(m * size_t(n) * r * 2);
     L.grad = take(m * size_t(n) * size_t(N) * 2);
-    L.sums = take(size_t(n) * down_sum_bytes(r));
+    L.sums = take(act_down_sum_bytes(n, r, sms));
     L.bias = take(n == 1 ? (m + 127) / 128 * size_t(N) * 4 : 0);
   }
   L.partial = off;
   size_t pb = narrow_partial_bytes(M, sms);
   if (bwd && n == 1 && M > 0 && M <= shortk::kMaxRows) pb = std::max(pb, short_plan(N, K, M, true, sms).partial_bytes);
   if (bwd && n == 1 && use_stream(M, 1)) pb = std::max(pb, stream_plan(N, K, M, true, sms).partial_bytes);
+  // (a batch the narrow, short-batch or streaming kernels take needs no split accumulators)
+  const size_t any = ~size_t(0);
+  if (M > narrow::kMaxRows) pb = std::max(pb, split_fwd(N, K, M, r, n, sms, any).bytes);
+  if (bwd) pb = std::max(pb, split_dx(N, K, M, r, n, sms, any).bytes);
   take(pb);
   L.total = off;
   return L;

@@ -47,6 +47,7 @@
 namespace qlora {
 namespace narrow {
 constexpr int kMaxRows = 16;
+constexpr int kMaxDownRows = 64;           // of the down-projection
 constexpr int kWarps = 16;                 // decoding warps
 constexpr int kXWarps = 1;                 // brings X
 constexpr int kEpiWarps = 3;               // finish tiles

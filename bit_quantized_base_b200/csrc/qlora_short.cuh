@@ -95,7 +95,6 @@ struct ShortParams {
   int iters;                         // L: iterations per CTA
   int max_pieces;
   float ts_mul;                      // 2^8 for NVFP4, else 1
-  int act_late;                      // the activations come from the previous kernel: wait for it first
   uint32_t one;                      // 1 (see decode_mul)
   uint32_t zero;                     // 0 (see zero_after)
 };
@@ -218,7 +217,7 @@ qlora_short_fwd_kernel(const __grid_constant__ ShortParams p) {
       uint32_t s = 0, ph = 0;
       int st = g0 % nk1;
       for (int g = g0; g < g1; ++g) {
-        if ((st == nk || p.act_late) && !waited) {
+        if (st == nk && !waited) {
           ptx::griddep_wait();
           waited = true;
         }
@@ -570,7 +569,7 @@ qlora_short_dx_kernel(const __grid_constant__ ShortParams p) {
       uint32_t s = 0, ph = 0;
       int st = g0 % nk1;
       for (int g = g0; g < g1; ++g) {
-        if ((st == nk || p.act_late) && !waited) {
+        if (st == nk && !waited) {
           ptx::griddep_wait();
           waited = true;
         }

@@ -80,7 +80,6 @@ struct StreamParams {
   int xrows;                         // M rounded up to 16: activation rows per stage, MMA N
   uint32_t zero;                     // 0 (see zero_after)
   int segments;                      // partial segments the workspace holds
-  int act_late;                      // the activations come from the previous kernel: wait for it first
 };
 
 // Segments are the pieces of the iteration space between consecutive CTA-range starts (multiples
@@ -170,7 +169,7 @@ qlora_stream_gemm_kernel(const __grid_constant__ StreamParams p) {
       int ks = rg.step(rg.g0);
       bool waited = false;
       for (int g = rg.g0; g < rg.g1; ++g) {
-        if ((ks == nk || p.act_late) && !waited) {
+        if (ks == nk && !waited) {
           ptx::griddep_wait();
           waited = true;
         }

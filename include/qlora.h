@@ -466,7 +466,8 @@ QLORA_API qlora_status_t qlora_debug_decode_rate(int fmt, int iters,
  * "fused_dx", "lora_down_T", "lora_down_U", "lora_wgrad" (grouped variants add "grouped_"),
  * "stream_fwd", "stream_dx", "stream_reduce" (batches of 65-256 rows), "short_fwd", "short_dx"
  * (batches of up to 64 rows), "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma",
- * "gated_fwd", "gated_dx", "act_fwd", "act_down" (gradients behind an activation), "bias_sum".
+ * "gated_fwd", "gated_dx", "act_fwd", "act_down" (gradients behind an activation), "bias_sum",
+ * "narrow_down_T" (batches of up to 16 rows), "split_sum".
  * Host-side bookkeeping only; the compute path is unchanged when profiling is off. */
 QLORA_API int64_t qlora_launch_count(void);
 QLORA_API qlora_status_t qlora_profile_enable(int enable);
