@@ -392,14 +392,14 @@ enum Kind : int {
   kKindStreamFwd, kKindStreamDx, kKindStreamReduce, kKindShortFwd, kKindShortDx,
   kKindW4a8Quant, kKindW4a8Gemm, kKindNormFwd, kKindNormBwd, kKindNormDgamma,
   kKindGatedFwd, kKindGatedDx, kKindActFwd, kKindActDown, kKindBiasSum,
-  kKindNarrowDown, kKindSplit, kNumKinds
+  kKindNarrowDown, kKindSplit, kKindDownSum, kNumKinds
 };
 const char* const kKindNames[kNumKinds] = {
     "fused_fwd", "fused_dx", "lora_down_T", "lora_down_U", "lora_wgrad",
     "grouped_fused_fwd", "grouped_fused_dx", "grouped_lora_down_T", "grouped_lora_down_U",
     "grouped_lora_wgrad", "stream_fwd", "stream_dx", "stream_reduce", "short_fwd", "short_dx",
     "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma",
-    "gated_fwd", "gated_dx", "act_fwd", "act_down", "bias_sum", "narrow_down_T", "split_sum"};
+    "gated_fwd", "gated_dx", "act_fwd", "act_down", "bias_sum", "narrow_down_T", "split_sum", "down_sum"};
 constexpr int kMaxProfiled = 65536;
 
 std::atomic<int64_t> g_launches{0};
@@ -735,16 +735,17 @@ qlora_status_t launch_short(const qlora_weight_t* W, bool dx, const void* act, c
 // A second weight's adapter gradients in the same launch (the same X, N, K and r; one expert).
 // mul, div: dY is stored times mul / div.
 struct WgradSecond {
-  const void *dY, *T, *U;
+  const void *dY, *T, *U, *U_lo;
   void *dA, *dB;
   const float *mul, *div;
 };
 
-// dB [E, N, r] = s dY_e^T T_e and dA [E, r, K] = s U_e^T X_e over each expert's rows.
+// dB [E, N, r] = s dY_e^T T_e and dA [E, r, K] = s U_e^T X_e over each expert's rows.  U_lo: what
+// rounding left out of U, multiplied too.
 qlora_status_t launch_wgrad(const void* X, const void* dY, const void* T, const void* U, int64_t M,
                             int64_t N, int64_t K, int r, float s, void* dA, void* dB, void* ws,
                             const int32_t* offsets, int E, bool grouped, cudaStream_t st,
-                            const WgradSecond* second = nullptr) {
+                            const void* U_lo = nullptr, const WgradSecond* second = nullptr) {
   WgradParams p{};
   const int rpad = rank_pad(r);
   const int nw = second ? 2 : 1;
@@ -762,6 +763,9 @@ qlora_status_t launch_wgrad(const void* X, const void* dY, const void* T, const 
     return QLORA_ERR_CUDA;
   p.out[0] = static_cast<__nv_bfloat16*>(dB);
   p.out[1] = static_cast<__nv_bfloat16*>(dA);
+  if (U_lo && !tmap_2d(&p.tm_r2[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, U_lo, uint64_t(r), rows, uint64_t(r) * 2,
+                       uint32_t(rpad), 64, rsw))
+    return QLORA_ERR_CUDA;
   if (second) {
     p.tm_l[3] = p.tm_l[1];
     if (!tmap_2d(&p.tm_l[2], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, second->dY, uint64_t(N), rows,
@@ -773,6 +777,9 @@ qlora_status_t launch_wgrad(const void* X, const void* dY, const void* T, const 
       return QLORA_ERR_CUDA;
     p.out[2] = static_cast<__nv_bfloat16*>(second->dB);
     p.out[3] = static_cast<__nv_bfloat16*>(second->dA);
+    if (U_lo && !tmap_2d(&p.tm_r2[1], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, second->U_lo, uint64_t(r), rows,
+                         uint64_t(r) * 2, uint32_t(rpad), 64, rsw))
+      return QLORA_ERR_CUDA;
     p.l2_mul = second->mul;
     p.l2_div = second->div;
   }
@@ -789,12 +796,12 @@ qlora_status_t launch_wgrad(const void* X, const void* dY, const void* T, const 
   p.E = E;
   p.s = s;
   p.nw = nw;
-  const size_t smem = lora::smem_bytes(E);
-  if (!set_smem(qlora_lora_wgrad_kernel, smem)) return QLORA_ERR_CUDA;
+  const size_t smem = lora::wgrad_smem_bytes(U_lo != nullptr, E);
+  auto kern = U_lo ? qlora_lora_wgrad_kernel<true> : qlora_lora_wgrad_kernel<false>;
+  if (!set_smem(kern, smem)) return QLORA_ERR_CUDA;
   const unsigned grid = unsigned(int64_t(E) * nw * (wp.tiles0 + wp.tiles1) * wp.S);
   LaunchScope scope(grouped ? kKindGWgrad : kKindWgrad, st);
-  if (launch_pdl_cluster(qlora_lora_wgrad_kernel, dim3(grid), dim3(lora::kThreads), smem, st, p,
-                         unsigned(wp.S)) != cudaSuccess)
+  if (launch_pdl_cluster(kern, dim3(grid), dim3(lora::kThreads), smem, st, p, unsigned(wp.S)) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }

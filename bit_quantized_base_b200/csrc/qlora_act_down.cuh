@@ -8,20 +8,18 @@
 // projection multiplies them while they are on the chip.  Memory bound: 3 reads and 2 writes (NB =
 // 2) of an [M, N] bf16 tensor, which a separate elementwise kernel would follow with 2 more reads.
 //
-// The projection takes each gradient as the sum of two bf16 values (the rounded gradient and the
-// rest of its binary32 value), two MMAs into one accumulator: U then carries no rounding of the
-// gradient, and dA = s U^T X, a product of U, only U's own.
+// U leaves as the sum of two bf16 tensors, its rounded value and the rest: dA = s U^T X multiplies both
+// (qlora_lora_wgrad_kernel<true>), so that the roundings of dA are the gradient's and its own.
 //
-// Work split: 128-row tiles; the N columns of a tile are split over S CTAs of one cluster (partial
-// sums added in split order through distributed shared memory) times C clusters, whose sums go to
-// the workspace and are added in cluster order by the last to arrive.  S C tiles fill the SMs twice:
-// two CTAs share an SM, so that one computes while the other waits for its loads or its MMAs (one CTA
-// per SM with two operand stages took 176 us where this one takes 110, at 4096 x 14336; 91 us of
-// traffic at the copy rate).
+// Work split: 128-row tiles, the N columns of a tile over S CTAs (about two per SM in all, at least
+// two 64-column chunks each); every CTA writes its binary32 sums to the workspace and
+// qlora_down_sum_kernel adds them in split order.  (Clusters of CTAs adding through distributed
+// shared memory took 6 to 10 us for that at rank 64, most of a short batch's time.)
 //
-// 256 threads: all load (one 64-column chunk ahead, in registers), differentiate, and write the
-// gradients and the swizzled operand tiles; one thread also copies the chunks' rows of B (TMA) and
-// issues the MMAs; at the end four warps drain the accumulators.
+// 256 threads, two CTAs per SM: all load (one 64-column chunk ahead, in registers), differentiate, and
+// write the gradients and the swizzled operand tiles (two stages); one thread also copies the chunks'
+// rows of B (TMA) and issues the MMAs, a chunk behind so that it never waits for the other warps; at
+// the end four warps drain the accumulators.
 #pragma once
 #include <cuda_bf16.h>
 #include "qlora_ptx.cuh"
@@ -37,36 +35,22 @@ constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kRowStep = kWarps * 4;            // rows between two vectors of a thread
 constexpr int kTmemCols = 128;                  // accumulator of stream b at column 64 b
 constexpr int kVec = BM * BK / 8 / kThreads;    // 16-byte vectors a thread holds per tensor
-constexpr int kMaxTilesSplit = 240;             // counters: [tiles][S] of them when C > 1
-// operand tiles of one chunk, two chunks' rows of B, barriers, bias partials
+// two stages of operand tiles and rows of B, barriers, bias partials
 __host__ __device__ constexpr size_t smem_bytes(int nb) {
-  return 1024 + size_t(nb) * (2 * T_BYTES + 2 * R_BYTES) + 256 + kWarps * 256;
+  return 1024 + size_t(2 * nb) * (T_BYTES + R_BYTES) + 256 + kWarps * 256;
 }
 
-// What rounding x0, x1 to the bf16 pair `hi` left out, as a bf16 pair (0 where `hi` is infinite or NaN:
-// the value is all there).
-__device__ __forceinline__ uint32_t rest2(uint32_t hi, float x0, float x1) {
-  const uint32_t lo = ptx::cvt_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xFFFF0000u));
-  const uint32_t top = ((hi & 0x7F807F80u) + 0x00800080u) & 0x80008000u;   // halves with a full exponent
-  if (top == 0u) return lo;
-  return lo & ~((top >> 15) * 0xFFFFu);
-}
 }  // namespace actdown
 
 struct ActDownParams {
   CUtensorMap tm_r[2];               // B of each stream: [1, N, r], box {rpad, 64, 1}
   const __nv_bfloat16 *dy, *a0, *a1; // gated: dH, G, U; plain: dY, Z (or null: act none)
   __nv_bfloat16* grad[2];            // [M, N] out: dG, dU / dZ (or null: dZ is dY itself)
-  __nv_bfloat16* z[2];               // [M, r] out: U of each stream
-  __nv_bfloat16* zs;                 // [M, ldzs] out: the dX kernel's LoRA operand, stream b at column b r
+  float* part;                       // [S][M][NB r] out: the splits' sums, stream b at column b r
   const float *ts0, *ts1;            // NVFP4: tensor scales of the streams' weights, else null
   float* bias_part;                  // NB = 1: [tiles][N] partial column sums, or null
   int* status;
-  float* cpart;                      // C > 1: [tiles][C][NB][128][rpad] fp32
-  unsigned* ccount;                  // C > 1: [tiles][S] arrival counters, zero between launches
-  int M, N, r, rpad, ldzs, num_k, S, C, sps;
-  float s;
-  float zs_mul;                      // as DownParams
+  int M, N, r, rpad, num_k, S, sps;
 };
 
 template <int NB, int ACT>
@@ -76,33 +60,33 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* tail = smem + size_t(NB) * (2 * T_BYTES + 2 * R_BYTES);
+  uint8_t* tail = smem + size_t(2 * NB) * (T_BYTES + R_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(tail);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile unsigned* s_ticket = reinterpret_cast<volatile unsigned*>(tmem_slot + 2);
   float* s_bias = reinterpret_cast<float*>(tail + 256);          // [kWarps][64]
   const uint32_t b0 = ptx::smem_u32(bars);
-  const uint32_t full = b0, empty = b0 + 8u, acc_full = b0 + 16u;    // operand tiles written / multiplied
-  auto b_full = [&](int q) { return b0 + 24u + 8u * uint32_t(q); };   // rows of B of an even / odd chunk
-  // stream b's rounded tile, the rest's tile; its rows of B
-  auto tile = [&](int b, int lo) { return ptx::smem_u32(smem) + uint32_t(2 * b + lo) * T_BYTES; };
-  auto rtile = [&](int q, int b) {
-    return ptx::smem_u32(smem) + uint32_t(2 * NB) * T_BYTES + uint32_t(q * NB + b) * R_BYTES;
+  // per stage q = chunk % 2: operand tiles written, multiplied; rows of B there
+  auto full = [&](uint32_t q) { return b0 + 8u * q; };
+  auto empty = [&](uint32_t q) { return b0 + 16u + 8u * q; };
+  auto b_full = [&](uint32_t q) { return b0 + 32u + 8u * q; };
+  const uint32_t acc_full = b0 + 48u;
+  auto tile = [&](uint32_t q, int b) { return ptx::smem_u32(smem) + (q * NB + uint32_t(b)) * uint32_t(T_BYTES); };
+  auto rtile = [&](uint32_t q, int b) {
+    return ptx::smem_u32(smem) + uint32_t(2 * NB * T_BYTES) + (q * NB + uint32_t(b)) * uint32_t(R_BYTES);
   };
 
-  const int per_tile = p.S * p.C;
-  const int mt = int(blockIdx.x) / per_tile, gs = int(blockIdx.x) % per_tile;
-  const int split = gs % p.S, cg = gs / p.S;
+  const int mt = int(blockIdx.x) / p.S, split = int(blockIdx.x) % p.S;
   const int m0 = mt * BM;
-  const int ks0 = min(gs * p.sps, p.num_k), ks1 = min(ks0 + p.sps, p.num_k);
+  const int ks0 = split * p.sps, ks1 = min(ks0 + p.sps, p.num_k);   // never empty
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    ptx::mbar_init(full, kWarps);
-    ptx::mbar_init(empty, 1);
+    for (uint32_t q = 0; q < 2; ++q) {
+      ptx::mbar_init(full(q), kWarps);
+      ptx::mbar_init(empty(q), 1);
+      ptx::mbar_init(b_full(q), 1);
+    }
     ptx::mbar_init(acc_full, 1);
-    ptx::mbar_init(b_full(0), 1);
-    ptx::mbar_init(b_full(1), 1);
     *abort_flag = 0;
     ptx::fence_mbarrier_init();
   }
@@ -121,29 +105,31 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
   const float ts0 = p.ts0 ? __ldg(p.ts0) : 1.0f;
   // dX has one accumulator, scaled by the first weight's tensor scale at the end
   const float up_ratio = NB == 2 && p.ts1 ? __ldg(p.ts1) / ts0 : 1.0f;
-  const float zscale = p.s / ts0 * p.zs_mul;
-  auto write8 = [&](int b, int rw, int c, const float (&v)[8]) {
-    if (c >= p.r) return;
-    if (!ptx::dcheck(rw >= 0 && rw < p.M, p.status)) return;
-    uint4 z, zs;
-    z.x = ptx::cvt_bf16x2(v[0], v[1]); z.y = ptx::cvt_bf16x2(v[2], v[3]);
-    z.z = ptx::cvt_bf16x2(v[4], v[5]); z.w = ptx::cvt_bf16x2(v[6], v[7]);
-    zs.x = ptx::cvt_bf16x2(v[0] * zscale, v[1] * zscale);
-    zs.y = ptx::cvt_bf16x2(v[2] * zscale, v[3] * zscale);
-    zs.z = ptx::cvt_bf16x2(v[4] * zscale, v[5] * zscale);
-    zs.w = ptx::cvt_bf16x2(v[6] * zscale, v[7] * zscale);
-    *reinterpret_cast<uint4*>(p.z[b] + size_t(rw) * p.r + c) = z;
-    *reinterpret_cast<uint4*>(p.zs + size_t(rw) * p.ldzs + size_t(b) * p.r + c) = zs;
-  };
-
   auto copy_b = [&](int ks) {
-    const int q = (ks - ks0) & 1;
+    const uint32_t q = uint32_t(ks - ks0) & 1u;
     ptx::mbar_arrive_expect_tx(b_full(q), uint32_t(NB) * r_bytes);
     for (int b = 0; b < NB; ++b) ptx::tma_load_3d(rtile(q, b), &p.tm_r[b], b_full(q), 0, ks * BK, 0);
   };
   const uint32_t idesc = ptx::idesc_bf16(128, uint32_t(p.rpad), 0u, 1u);
   const uint32_t rsw = swz_mode_for_row_bytes(rowb);
-  if (threadIdx.x == 0 && ks1 > ks0) copy_b(ks0);
+  // thread 0: the MMAs of chunk n, whose tiles every warp has written or is about to
+  auto multiply = [&](uint32_t n) {
+    const uint32_t q = n & 1u, ph = (n >> 1) & 1u;
+    if (!ptx::mbar_wait(full(q), ph, p.status, abort_flag) || !ptx::mbar_wait(b_full(q), ph, p.status, abort_flag))
+      return;
+    ptx::tc_fence_after();
+    for (int b = 0; b < NB; ++b)
+      for (int kk = 0; kk < BK / 16; ++kk) {
+        const uint64_t ad = ptx::smem_desc(tile(q, b) + kk * 32, 16, 1024, ptx::kSw128);
+        const uint64_t bd = ptx::smem_desc(rtile(q, b) + kk * 16 * rowb, 64 * rowb, 8 * rowb, rsw);
+        ptx::mma_bf16(tmem + uint32_t(b) * 64u, ad, bd, idesc, (n > 0 || kk > 0) ? 1u : 0u);
+      }
+    ptx::mma_commit(empty(q));
+  };
+  if (threadIdx.x == 0) {
+    copy_b(ks0);
+    if (ks0 + 1 < ks1) copy_b(ks0 + 1);
+  }
   {
     // ---------------------------------------------------------------- gradients and operand tiles
     // Vector i of this thread: row vr + kRowStep i of the tile, columns 8 vc .. 8 vc + 7 of the chunk (a
@@ -170,11 +156,12 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
     for (int i = 0; i < kVec; ++i) load(ks0, i);
     for (int ks = ks0; ks < ks1; ++ks) {
       const uint32_t n = uint32_t(ks - ks0);
-      // the chunk before has been multiplied: its operand tiles and its rows of B are free  (a wait
-      // that gave up skips the shared-memory writes but not the barriers below, which all warps
-      // must reach)
-      const bool stage_ok = ptx::mbar_wait(empty, (n & 1u) ^ 1u, p.status, abort_flag);
-      if (threadIdx.x == 0 && stage_ok && ks + 1 < ks1) copy_b(ks + 1);
+      const uint32_t q = n & 1u;
+      // the chunk before last has been multiplied: its operand tiles and rows of B are free (a wait
+      // that gave up skips the shared-memory writes but not the barriers below, which all warps must
+      // reach)
+      const bool stage_ok = ptx::mbar_wait(empty(q), ((n >> 1) & 1u) ^ 1u, p.status, abort_flag);
+      if (threadIdx.x == 0 && stage_ok && n >= 2) copy_b(ks);
       float bsum[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) bsum[j] = 0.0f;
@@ -184,7 +171,7 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
         const uint32_t wg[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
         uint32_t wu[4] = {0u, 0u, 0u, 0u};
         if constexpr (NB == 2) { wu[0] = u[i].x; wu[1] = u[i].y; wu[2] = u[i].z; wu[3] = u[i].w; }
-        uint32_t hi[NB][4], lo[NB][4], out1[4];
+        uint32_t hi[NB][4], out1[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float x0, x1, y0, y1;
@@ -194,10 +181,8 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
                     __uint_as_float(wu[j] & 0xFFFF0000u), x1, y1);
           if constexpr (NB == 1) { bsum[2 * j] += x0; bsum[2 * j + 1] += x1; }
           hi[0][j] = ptx::cvt_bf16x2(x0, x1);
-          lo[0][j] = rest2(hi[0][j], x0, x1);
           if constexpr (NB == 2) {
             hi[1][j] = ptx::cvt_bf16x2(y0, y1);
-            lo[1][j] = rest2(hi[1][j], y0, y1);
             out1[j] = p.ts1 ? ptx::cvt_bf16x2(y0 * up_ratio, y1 * up_ratio) : hi[1][j];
           }
         }
@@ -206,8 +191,7 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
         const uint32_t off = uint32_t(lr) * 128u + ((uint32_t(vc) ^ (uint32_t(lr) & 7u)) << 4);
 #pragma unroll
         for (int b = 0; b < NB && stage_ok; ++b) {
-          ptx::st_shared_v4(tile(b, 0) + off, hi[b][0], hi[b][1], hi[b][2], hi[b][3]);
-          ptx::st_shared_v4(tile(b, 1) + off, lo[b][0], lo[b][1], lo[b][2], lo[b][3]);
+          ptx::st_shared_v4(tile(q, b) + off, hi[b][0], hi[b][1], hi[b][2], hi[b][3]);
         }
         if (row < p.M && col < p.N) {
           const size_t o = size_t(row) * p.N + col;
@@ -219,21 +203,8 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0 && stage_ok) ptx::mbar_arrive(full);
-      if (threadIdx.x == 0 && stage_ok && ptx::mbar_wait(full, n & 1u, p.status, abort_flag) &&
-          ptx::mbar_wait(b_full(int(n & 1u)), (n >> 1) & 1u, p.status, abort_flag)) {
-        ptx::tc_fence_after();
-        for (int b = 0; b < NB; ++b)
-          for (int lo = 0; lo < 2; ++lo)
-            for (int kk = 0; kk < BK / 16; ++kk) {
-              const uint64_t ad = ptx::smem_desc(tile(b, lo) + kk * 32, 16, 1024, ptx::kSw128);
-              const uint64_t bd =
-                  ptx::smem_desc(rtile(int(n & 1u), b) + kk * 16 * rowb, 64 * rowb, 8 * rowb, rsw);
-              ptx::mma_bf16(tmem + uint32_t(b) * 64u, ad, bd, idesc, (n > 0 || lo > 0 || kk > 0) ? 1u : 0u);
-            }
-        ptx::mma_commit(empty);
-        if (ks + 1 == ks1) ptx::mma_commit(acc_full);
-      }
+      if (lane == 0 && stage_ok) ptx::mbar_arrive(full(q));
+      if (threadIdx.x == 0 && n > 0) multiply(n - 1);
       __syncwarp();
       if constexpr (NB == 1) {
         if (p.bias_part) {
@@ -259,89 +230,27 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
     }
   }
 
-  // ------------------------------------------------------------------ accumulators to U and Zs
-  const bool have = ks1 > ks0;
-  const int nrows = min(BM, p.M - m0);
-  const uint32_t part = ptx::smem_u32(smem);       // the operand tiles are free by then: stream b at
-  constexpr uint32_t PART = 32768u;                // b * PART
-  if (warp < 4) {
-    if (have) ptx::mbar_wait(acc_full, 0, p.status, abort_flag);
-    ptx::named_bar_sync(2, 128);
-    if (*abort_flag == 0) {
-#pragma unroll 1
-      for (int b = 0; b < NB; ++b) {
-        float acc[64];
-        if (have) {
-          ptx::tc_fence_after();
-          load_acc_row(tmem + (uint32_t(warp * 32) << 16) + uint32_t(b) * 64u, p.rpad, acc);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) acc[c] = 0.0f;
-        }
-        if (p.S == 1 && p.C == 1) {
-          const int lr = warp * 32 + lane;
-          if (lr < nrows) {
-#pragma unroll
-            for (int c = 0; c < 64; c += 8) {
-              float v[8];
-#pragma unroll
-              for (int q = 0; q < 8; ++q) v[q] = acc[c + q];
-              write8(b, m0 + lr, c, v);
-            }
-          }
-        } else {
-          store_partial_row(part + uint32_t(b) * PART, warp * 32 + lane, acc, p.rpad);
-        }
-      }
-    }
+  // ------------------------------------------------------------------ sums of this split
+  if (threadIdx.x == 0) {
+    multiply(uint32_t(ks1 - ks0 - 1));
+    ptx::mma_commit(acc_full);
   }
-  if (p.S > 1 || p.C > 1) {
-    float* const csum = p.cpart + (size_t(mt) * p.C + cg) * NB * BM * p.rpad;
-    ptx::cluster_sync();
-    if (warp < 4 && *abort_flag == 0) {
+  __syncwarp();
+  if (warp < 4) {
+    const bool ok = ptx::mbar_wait(acc_full, 0, p.status, abort_flag);
+    __syncwarp();
+    ptx::tc_fence_after();
+    const int row = m0 + warp * 32 + lane;
+    float* dst = p.part + (size_t(split) * p.M + size_t(row)) * size_t(NB * p.r);
 #pragma unroll 1
-      for (int b = 0; b < NB; ++b) {
-        if (p.C == 1)
-          cluster_sum(part + uint32_t(b) * PART, p.rpad, p.S, split, nrows, int(threadIdx.x),
-                      [&](int lr, int c, const float (&v)[8]) { write8(b, m0 + lr, c, v); });
-        else
-          cluster_sum(part + uint32_t(b) * PART, p.rpad, p.S, split, nrows, int(threadIdx.x),
-                      [&](int lr, int c, const float (&v)[8]) {
-                        float4* dst = reinterpret_cast<float4*>(csum + (size_t(b) * BM + lr) * p.rpad + c);
-                        __stcg(dst, make_float4(v[0], v[1], v[2], v[3]));
-                        __stcg(dst + 1, make_float4(v[4], v[5], v[6], v[7]));
-                      });
-      }
-    }
-    ptx::cluster_sync();
-    if (p.C > 1 && warp < 4) {
-      unsigned* const counter = p.ccount + mt * p.S + split;
-      __threadfence();
-      ptx::named_bar_sync(2, 128);
-      if (threadIdx.x == 0) *s_ticket = atomicAdd(counter, 1u);
-      ptx::named_bar_sync(2, 128);
-      if (*s_ticket == unsigned(p.C - 1)) {
-        __threadfence();
-        const int rows_per = (BM + p.S - 1) / p.S;
-        const int r0 = split * rows_per, r1 = min(nrows, r0 + rows_per);
-        const int g8 = p.rpad / 8;
-        const int items = r1 > r0 ? (r1 - r0) * g8 * NB : 0;
-        for (int it = int(threadIdx.x); it < items && *abort_flag == 0; it += 128) {
-          const int b = it / ((r1 - r0) * g8), q = it % ((r1 - r0) * g8);
-          const int lr = r0 + q / g8, c = (q % g8) * 8;
-          float v[8];
+    for (int b = 0; b < NB; ++b) {
+      float acc[64];
+      load_acc_row(tmem + (uint32_t(warp * 32) << 16) + uint32_t(b) * 64u, p.rpad, acc);
+      if (ok && row < p.M && *abort_flag == 0) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-          for (int k = 0; k < p.C; ++k) {
-            const float4* src = reinterpret_cast<const float4*>(
-                p.cpart + (((size_t(mt) * p.C + k) * NB + b) * BM + lr) * p.rpad + c);
-            const float4 x = __ldcg(src), y = __ldcg(src + 1);
-            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-          }
-          write8(b, m0 + lr, c, v);
-        }
-        if (threadIdx.x == 0) *counter = 0u;
+        for (int c = 0; c < 64; c += 4)
+          if (c < p.r)
+            *reinterpret_cast<float4*>(dst + b * p.r + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
       }
     }
   }
@@ -349,6 +258,60 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
   __syncthreads();
   ptx::tc_fence_after();
   if (warp == 0) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+// U of each stream from the splits' sums, in split order: 32 groups of 4 columns a CTA, 8 slices of
+// the splits each, added in slice order.  Writes U as hi + lo and the dX kernel's operand Zs.
+struct DownSumParams {
+  const float* part;                 // [S][M][width], stream b at column b r
+  __nv_bfloat16 *hi[2], *lo[2];      // [M, r] each
+  __nv_bfloat16* zs;                 // [M, width] = bf16(U s zs_mul / ts)
+  const float* ts;                   // the first weight's tensor scale, or null
+  long long groups;                  // M * width / 4
+  int S, r, width;
+  float s, zs_mul;                   // zs_mul: as DownParams
+};
+__global__ void __launch_bounds__(256) qlora_down_sum_kernel(const __grid_constant__ DownSumParams p) {
+  __shared__ float4 sm[8][32];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int c = int(threadIdx.x) & 31, sl = int(threadIdx.x) >> 5;
+  const long long q = (long long)blockIdx.x * 32 + c;
+  const int per = (p.S + 7) / 8;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (q < p.groups) {
+    const float4* src = reinterpret_cast<const float4*>(p.part) + q;
+    const int s1 = min(p.S, (sl + 1) * per);
+#pragma unroll 4
+    for (int k = sl * per; k < s1; ++k) {
+      const float4 v = __ldcg(src + size_t(k) * size_t(p.groups));
+      a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+    }
+  }
+  sm[sl][c] = a;
+  __syncthreads();
+  if (sl != 0 || q >= p.groups) return;
+  for (int k = 1; k < 8 && k * per < p.S; ++k) {
+    const float4 v = sm[k][c];
+    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+  }
+  const long long row = q * 4 / p.width;
+  const int col = int(q * 4 - row * p.width);
+  const int b = col >= p.r ? 1 : 0;
+  const size_t o = size_t(row) * p.r + (col - b * p.r);
+  const uint32_t h0 = ptx::cvt_bf16x2(a.x, a.y), h1 = ptx::cvt_bf16x2(a.z, a.w);
+  // (an infinite or NaN sum is all in hi)
+  auto rest = [](float x, uint32_t h16) {
+    const float d = x - __uint_as_float(h16 << 16);
+    return d - d == 0.0f ? d : 0.0f;
+  };
+  *reinterpret_cast<uint2*>(p.hi[b] + o) = make_uint2(h0, h1);
+  *reinterpret_cast<uint2*>(p.lo[b] + o) =
+      make_uint2(ptx::cvt_bf16x2(rest(a.x, h0 & 0xFFFFu), rest(a.y, h0 >> 16)),
+                 ptx::cvt_bf16x2(rest(a.z, h1 & 0xFFFFu), rest(a.w, h1 >> 16)));
+  const float zs = p.s / (p.ts ? __ldg(p.ts) : 1.0f) * p.zs_mul;
+  *reinterpret_cast<uint2*>(p.zs + size_t(row) * p.width + col) =
+      make_uint2(ptx::cvt_bf16x2(a.x * zs, a.y * zs), ptx::cvt_bf16x2(a.z * zs, a.w * zs));
 }
 
 // dbias[n] = the sum over the row tiles of their partial column sums, in tile order.

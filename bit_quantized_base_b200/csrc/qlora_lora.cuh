@@ -343,10 +343,21 @@ qlora_lora_down_kernel(const __grid_constant__ DownParams p) {
   if (warp == 1) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
+// TWO: the R of dA comes as the sum of two tensors (tm_r2), both multiplied: 6 stages, twice the R bytes.
+namespace lora {
+__host__ __device__ constexpr int wgrad_stages(bool two) { return two ? 6 : NS; }
+__host__ __device__ constexpr int wgrad_r_bytes(bool two) { return two ? 2 * R_BYTES : R_BYTES; }
+__host__ __device__ constexpr size_t wgrad_base(bool two) {
+  return 1024 + size_t(wgrad_stages(two)) * (A_BYTES + wgrad_r_bytes(two)) + 512;
+}
+__host__ __device__ constexpr size_t wgrad_smem_bytes(bool two, int E) { return wgrad_base(two) + size_t(2) * (E + 1) * 4; }
+}  // namespace lora
+
 struct WgradParams {
   // problems 0 and 1: dB and dA; 2 and 3 (nw = 2, one expert): the same of a second weight
   CUtensorMap tm_l[4];  // L: dY [M, N] (problem 0, dB) / X [M, K] (problem 1, dA); box {64, 64} SW128
   CUtensorMap tm_r[4];  // R: T [M, r] / U [M, r]; box {rpad, 64} SW(2 rpad)
+  CUtensorMap tm_r2[2]; // TWO: the rest of U, of each weight
   __nv_bfloat16* out[4];  // dB [E, N, r]: (p, j) at p * r + j; dA [E, r, K]: (p, j) at j * K + p
   const int32_t* offsets;       // grouped: device [E+1]; nullptr: one expert of M rows
   int* status;
@@ -356,9 +367,11 @@ struct WgradParams {
   const float *l2_mul, *l2_div;  // not null: L of problem 2 holds dY * l2_mul / l2_div, taken out here
 };
 
+template <bool TWO>
 __global__ void __launch_bounds__(lora::kThreads, 1)
 qlora_lora_wgrad_kernel(const __grid_constant__ WgradParams p) {
   using namespace lora;
+  constexpr int NS = wgrad_stages(TWO), R_BYTES = wgrad_r_bytes(TWO);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -367,7 +380,7 @@ qlora_lora_wgrad_kernel(const __grid_constant__ WgradParams p) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(rs + NS * R_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NS + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* s_off = reinterpret_cast<int*>(smem + (kSmemBase - 1024));
+  int* s_off = reinterpret_cast<int*>(smem + (wgrad_base(TWO) - 1024));
   int* s_first = s_off + (p.E + 1);
   const uint32_t b0 = ptx::smem_u32(bars);
   auto full = [&](uint32_t s) { return b0 + 8u * s; };
@@ -438,13 +451,15 @@ qlora_lora_wgrad_kernel(const __grid_constant__ WgradParams p) {
         const int it = ks - ks0;
         const uint32_t s = it % NS, ph = (it / NS) & 1;
         if (!ptx::mbar_wait(empty(s), ph ^ 1u, p.status, abort_flag)) break;
-        ptx::mbar_arrive_expect_tx(full(s), A_BYTES + r_bytes);
+        const bool two = TWO && side == 1;
+        ptx::mbar_arrive_expect_tx(full(s), A_BYTES + (two ? 2u : 1u) * r_bytes);
         const uint32_t ad = ptx::smem_u32(as + s * A_BYTES);
         const int m = row_begin + ks * BK;
         if (!ptx::dcheck(ptx::tma_x_ok(p0, 2) && m >= 0 && m < p.M, p.status)) break;
         ptx::tma_load_2d(ad, tml, full(s), p0, m);
         ptx::tma_load_2d(ad + A_BYTES / 2, tml, full(s), p0 + 64, m);
         ptx::tma_load_2d(ptx::smem_u32(rs + s * R_BYTES), tmr, full(s), 0, m);
+        if (two) ptx::tma_load_2d(ptx::smem_u32(rs + s * R_BYTES) + lora::R_BYTES, &p.tm_r2[prob >> 1], full(s), 0, m);
       }
     }
   } else if (warp == 1) {
@@ -479,6 +494,10 @@ qlora_lora_wgrad_kernel(const __grid_constant__ WgradParams p) {
             const uint64_t ad = ptx::smem_desc(a + kk * 2048, 8192, 1024, ptx::kSw128);
             const uint64_t bd = ptx::smem_desc(b + kk * 16 * rowb, 64 * rowb, 8 * rowb, rsw);
             ptx::mma_bf16(tmem, ad, bd, idesc, (it > 0 || kk > 0) ? 1u : 0u);
+            if (TWO && side == 1)
+              ptx::mma_bf16(tmem, ad,
+                            ptx::smem_desc(b + uint32_t(lora::R_BYTES) + kk * 16 * rowb, 64 * rowb, 8 * rowb, rsw),
+                            idesc, 1u);
           }
           ptx::mma_commit(empty(s));
         }

@@ -115,21 +115,21 @@ qlora_status_t launch_split(const FusedExParams& p, int n, bool gated, cudaStrea
 }
 
 template <int NB, int ACT>
-qlora_status_t launch_act_down_t(const ActDownParams& p, unsigned grid, unsigned cluster, cudaStream_t st) {
+qlora_status_t launch_act_down_t(const ActDownParams& p, unsigned grid, cudaStream_t st) {
   const size_t smem = actdown::smem_bytes(NB);
   if (!set_smem(qlora_act_down_kernel<NB, ACT>, smem)) return QLORA_ERR_CUDA;
   LaunchScope scope(kKindActDown, st);
-  if (launch_pdl_cluster(qlora_act_down_kernel<NB, ACT>, dim3(grid), dim3(actdown::kThreads), smem, st, p,
-                         cluster) != cudaSuccess)
+  if (launch_pdl(qlora_act_down_kernel<NB, ACT>, dim3(grid), dim3(actdown::kThreads), smem, st, p) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
-// Gradients of the pre-activations and their projections (nb = 1 or 2 streams).
+// Gradients of the pre-activations and their projections (nb = 1 or 2 streams): grad, U as u + u_lo, Zs.
 qlora_status_t launch_act_down(int nb, int act, const void* dy, const void* a0, const void* a1,
                                const void* const* B, const float* const* ts, void* const* grad,
-                               void* const* z, void* zs, float* bias_part, int64_t M, int64_t N, int r,
-                               float s, float zs_mul, void* sums, void* ws, cudaStream_t st) {
+                               void* const* u, void* const* u_lo, void* zs, float* bias_part, int64_t M,
+                               int64_t N, int r, float s, float zs_mul, void* sums, void* ws,
+                               cudaStream_t st) {
   ActDownParams p{};
   const int rpad = rank_pad(r);
   const ActDownPlan dp = act_down_plan(M, N, num_sms());
@@ -138,43 +138,55 @@ qlora_status_t launch_act_down(int nb, int act, const void* dy, const void* a0, 
                  swizzle_for_bytes(uint32_t(rpad) * 2)))
       return QLORA_ERR_CUDA;
     p.grad[b] = static_cast<__nv_bfloat16*>(grad[b]);
-    p.z[b] = static_cast<__nv_bfloat16*>(z[b]);
   }
   p.dy = static_cast<const __nv_bfloat16*>(dy);
   p.a0 = static_cast<const __nv_bfloat16*>(a0);
   p.a1 = static_cast<const __nv_bfloat16*>(a1);
-  p.zs = static_cast<__nv_bfloat16*>(zs);
+  p.part = static_cast<float*>(sums);
   p.ts0 = ts[0];
   p.ts1 = nb == 2 ? ts[1] : nullptr;
   p.bias_part = bias_part;
   p.status = ws_status(ws);
-  if (dp.C > 1) {
-    p.cpart = static_cast<float*>(sums);
-    p.ccount = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + kCounterOffset);
-  }
   p.M = int(M);
   p.N = int(N);
   p.r = r;
   p.rpad = rpad;
-  p.ldzs = nb * r;
   p.num_k = dp.num_k;
   p.S = dp.S;
-  p.C = dp.C;
   p.sps = dp.sps;
-  p.s = s;
-  p.zs_mul = zs_mul;
-  const unsigned grid = unsigned(dp.tiles * dp.S * dp.C);
-  const unsigned cl = unsigned(dp.S);
+  const unsigned grid = unsigned(int64_t(dp.tiles) * dp.S);
+  qlora_status_t rc;
   switch ((nb - 1) * act::kNumActs + act) {
-    case 0: return launch_act_down_t<1, act::kNone>(p, grid, cl, st);
-    case 1: return launch_act_down_t<1, act::kSilu>(p, grid, cl, st);
-    case 2: return launch_act_down_t<1, act::kGelu>(p, grid, cl, st);
-    case 3: return launch_act_down_t<1, act::kGeluTanh>(p, grid, cl, st);
-    case 4: return launch_act_down_t<2, act::kNone>(p, grid, cl, st);
-    case 5: return launch_act_down_t<2, act::kSilu>(p, grid, cl, st);
-    case 6: return launch_act_down_t<2, act::kGelu>(p, grid, cl, st);
-    default: return launch_act_down_t<2, act::kGeluTanh>(p, grid, cl, st);
+    case 0: rc = launch_act_down_t<1, act::kNone>(p, grid, st); break;
+    case 1: rc = launch_act_down_t<1, act::kSilu>(p, grid, st); break;
+    case 2: rc = launch_act_down_t<1, act::kGelu>(p, grid, st); break;
+    case 3: rc = launch_act_down_t<1, act::kGeluTanh>(p, grid, st); break;
+    case 4: rc = launch_act_down_t<2, act::kNone>(p, grid, st); break;
+    case 5: rc = launch_act_down_t<2, act::kSilu>(p, grid, st); break;
+    case 6: rc = launch_act_down_t<2, act::kGelu>(p, grid, st); break;
+    default: rc = launch_act_down_t<2, act::kGeluTanh>(p, grid, st); break;
   }
+  if (rc != QLORA_OK) return rc;
+  DownSumParams q{};
+  q.part = p.part;
+  for (int b = 0; b < nb; ++b) {
+    q.hi[b] = static_cast<__nv_bfloat16*>(u[b]);
+    q.lo[b] = static_cast<__nv_bfloat16*>(u_lo[b]);
+  }
+  q.zs = static_cast<__nv_bfloat16*>(zs);
+  q.ts = ts[0];
+  q.width = nb * r;
+  q.groups = (long long)M * (q.width / 4);
+  q.S = dp.S;
+  q.r = r;
+  q.s = s;
+  q.zs_mul = zs_mul;
+  if (!set_smem(qlora_down_sum_kernel, 0)) return QLORA_ERR_CUDA;
+  LaunchScope scope(kKindDownSum, st);
+  if (launch_pdl(qlora_down_sum_kernel, dim3(unsigned((q.groups + 31) / 32)), dim3(256), 0, st, q) != cudaSuccess ||
+      cudaGetLastError() != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  return QLORA_OK;
 }
 
 // Runs `side_work` on the device's side stream beside `main_work` on `s`, joined into `s` again.  The
@@ -425,14 +437,16 @@ qlora_status_t qlora_gated_mlp_bwd(const qlora_weight_t* Wg, const qlora_weight_
   }
   void* const grad[2] = {w + L.grad, w + L.grad + mn};
   void* const z[2] = {w + L.u, w + L.u + mr};
+  void* const z_lo[2] = {w + L.u_lo, w + L.u_lo + mr};
   const void* const Bs[2] = {Bg, Bu};
   const float* const ts[2] = {ts_of(Wg), ts_of(Wu)};
-  st = launch_act_down(2, act, dH, G, U, Bs, ts, grad, z, w + L.zs, nullptr, M, N, r, scale, 1.0f,
+  st = launch_act_down(2, act, dH, G, U, Bs, ts, grad, z, z_lo, w + L.zs, nullptr, M, N, r, scale, 1.0f,
                        w + L.sums, ws, s);
   if (st != QLORA_OK) return st;
   auto wgrads = [&](cudaStream_t q) {
-    const WgradSecond up{grad[1], Ts + mr, z[1], dAu, dBu, ts[1], ts[0]};
-    return launch_wgrad(X, grad[0], Ts, z[0], M, N, K, r, scale, dAg, dBg, ws, nullptr, 1, false, q, &up);
+    const WgradSecond up{grad[1], Ts + mr, z[1], z_lo[1], dAu, dBu, ts[1], ts[0]};
+    return launch_wgrad(X, grad[0], Ts, z[0], M, N, K, r, scale, dAg, dBg, ws, nullptr, 1, false, q, z_lo[0],
+                        &up);
   };
   if (!dX) return wgrads(s);
   return fork_join(s, wgrads, [&]() {
@@ -531,15 +545,16 @@ qlora_status_t qlora_linear_act_bwd(const qlora_weight_t* W, const void* X, cons
   }
   void* const grad[1] = {act == QLORA_ACT_NONE ? nullptr : w + L.grad};
   void* const z[1] = {w + L.u};
+  void* const z_lo[1] = {w + L.u_lo};
   const void* const Bs[1] = {B};
   const float* const ts[1] = {ts_of(W)};
   float* bias_part = dbias ? reinterpret_cast<float*>(w + L.bias) : nullptr;
-  st = launch_act_down(1, act, dY, act == QLORA_ACT_NONE ? nullptr : Z, nullptr, Bs, ts, grad, z, w + L.zs,
-                       bias_part, M, N, r, scale, short_dx ? short_zs_mul(W) : 1.0f, w + L.sums, ws, s);
+  st = launch_act_down(1, act, dY, act == QLORA_ACT_NONE ? nullptr : Z, nullptr, Bs, ts, grad, z, z_lo,
+                       w + L.zs, bias_part, M, N, r, scale, short_dx ? short_zs_mul(W) : 1.0f, w + L.sums, ws, s);
   if (st != QLORA_OK) return st;
   const void* dZ = act == QLORA_ACT_NONE ? dY : grad[0];
   auto side_work = [&](cudaStream_t q) {
-    const qlora_status_t e = launch_wgrad(X, dZ, T, z[0], M, N, K, r, scale, dA, dB, ws, nullptr, 1, false, q);
+    const qlora_status_t e = launch_wgrad(X, dZ, T, z[0], M, N, K, r, scale, dA, dB, ws, nullptr, 1, false, q, z_lo[0]);
     if (e != QLORA_OK || !dbias) return e;
     BiasSumParams b{bias_part, static_cast<__nv_bfloat16*>(dbias), int((M + 127) / 128), int(N)};
     LaunchScope scope(kKindBiasSum, q);

@@ -41,30 +41,30 @@ SplitPlan split_dx(int64_t N, int64_t K, int64_t M, int r, int n, int sms, size_
                     sms, room);
 }
 
-// The plan of the act_down kernel: S CTAs a cluster, C clusters a tile, two CTAs per SM, at least two
+// The plan of the act_down kernel: S CTAs a 128-row tile, about two CTAs per SM in all, at least two
 // 64-column chunks each.
 struct ActDownPlan {
-  int tiles, S, C, sps, num_k;
+  int tiles, S, sps, num_k;
 };
 ActDownPlan act_down_plan(int64_t M, int64_t N, int sms) {
   ActDownPlan p{};
   p.tiles = int((M + 127) / 128);
   p.num_k = int((N + 63) / 64);
-  int per = p.tiles > 0 ? 2 * sms / p.tiles : 1;               // CTAs a tile may have
-  per = std::max(1, std::min(per, p.num_k / 2));
-  p.S = std::min(per, kMaxClusterSplits);
-  p.C = p.S == kMaxClusterSplits && p.tiles <= actdown::kMaxTilesSplit ? per / p.S : 1;
-  p.sps = (p.num_k + p.S * p.C - 1) / (p.S * p.C);
+  const int most = std::max(1, std::min(p.tiles > 0 ? 2 * sms / p.tiles : 1, p.num_k / 2));
+  p.sps = (p.num_k + most - 1) / most;
+  p.S = (p.num_k + p.sps - 1) / p.sps;                          // no split is empty
   return p;
 }
-
-// Bytes of its cluster sums: C > 1 only with full clusters, so tiles * C <= 2 SMs / 8 whatever M.
-size_t act_down_sum_bytes(int nb, int r, int sms) {
-  return size_t(2 * sms / kMaxClusterSplits) * nb * 128 * size_t(rank_pad(r)) * 4;
+// Bytes that its sums take at most, for M rows and any fewer: S M <= 128 * 2 SMs, and S <= chunks / 2.
+size_t act_down_sum_bytes(int64_t M, int64_t N, int nb, int r, int sms) {
+  const int64_t num_k = (N + 63) / 64;
+  const int64_t rows = std::max(M, std::min(std::max<int64_t>(1, num_k / 2) * M, int64_t(256) * sms));
+  return size_t(rows > 0 ? rows : 0) * size_t(nb) * size_t(r) * 4;
 }
 
-// n = 2 (gated) or 1 weights.  header | Zs [M, n r] | T [n][M, r] | backward: U [n][M, r],
-// gradients of the pre-activations [n][M, N] bf16, the projection's cluster sums, bias partials
+// n = 2 (gated) or 1 weights.  header | Zs [M, n r] | T [n][M, r] | backward: U [n][M, r]
+// and the rest of its roundings [n][M, r], gradients of the pre-activations [n][M, N] bf16, the splits'
+// sums of U, bias partials
 // [ceil(M/128)][N] fp32 (n = 1), and the short-batch kernels' fp32 partials.
 // fp32 partials of the narrow kernel (batches of up to 16 rows): two pieces per CTA.
 size_t narrow_partial_bytes(int64_t M, int64_t sms) {
@@ -72,7 +72,7 @@ size_t narrow_partial_bytes(int64_t M, int64_t sms) {
 }
 
 struct MlpLayout {
-  size_t zs, t, u, grad, sums, bias, partial, total;
+  size_t zs, t, u, u_lo, grad, sums, bias, partial, total;
 };
 
 MlpLayout mlp_layout(int64_t N, int64_t K, int64_t M, int r, int n, bool bwd, int sms) {
@@ -88,8 +88,9 @@ MlpLayout mlp_layout(int64_t N, int64_t K, int64_t M, int r, int n, bool bwd, in
   L.t = take(m * size_t(n) * r * 2);
   if (bwd) {
     L.u = take(m * size_t(n) * r * 2);
+    L.u_lo = take(m * size_t(n) * r * 2);
     L.grad = take(m * size_t(n) * size_t(N) * 2);
-    L.sums = take(act_down_sum_bytes(n, r, sms));
+    L.sums = take(act_down_sum_bytes(M, N, n, r, sms));
     L.bias = take(n == 1 ? (m + 127) / 128 * size_t(N) * 4 : 0);
   }
   L.partial = off;

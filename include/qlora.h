@@ -318,8 +318,8 @@ QLORA_API qlora_status_t qlora_gated_mlp_fwd(const qlora_weight_t* Wg, const qlo
  * saved bf16 G and U):
  *   dX = dG deq(Wg) + dU deq(Wu) + s (dG Bg) Ag + s (dU Bu) Au
  *   dAg = s (dG Bg)^T X    dBg = s dG^T Tg    dAu = s (dU Bu)^T X    dBu = s dU^T Tu
- * dG and dU are rounded to bf16 as operands of the products with the weights and T; the rank-r
- * products dG Bg and dU Bu take them unrounded.
+ * dG and dU are rounded to bf16 as operands of every product; the rank-r products dG Bg and dU Bu
+ * enter dAg and dAu in two bf16 terms (2^-17), dX in one.
  *   T [2,M,r]: the forward's T_save, or NULL to recompute it from X, Ag and Au;
  *   G, U [M,N]: the forward's; dH [M,N]; dX [M,K] out or NULL; dAg, dAu [r,K], dBg, dBu [N,r] out;
  *   ws >= qlora_workspace_size(QLORA_OP_GATED_MLP_BWD, ...): holds dG and dU, 4 M N bytes.
@@ -350,7 +350,8 @@ QLORA_API qlora_status_t qlora_linear_act_fwd(const qlora_weight_t* W, const voi
 
 /* Backward of qlora_linear_act_fwd.  With dZ = dY act'(Z):
  *   dX = dZ deq(W) + s (dZ B) A    dA = s (dZ B)^T X    dB = s dZ^T T    dbias[n] = sum_m dZ[m,n]
- * (the residual's gradient is dY itself).  dbias and dZ B take dZ unrounded.
+ * (the residual's gradient is dY itself).  dZ is rounded to bf16 as the operand of the products, not
+ * for dbias; dZ B enters dA in two bf16 terms.
  *   T [M,r] or NULL (recomputed); Z [M,N]: the forward's Z_save, may be NULL for act NONE;
  *   dX [M,K] out or NULL; dA [r,K], dB [N,r] out; dbias [N] bf16 out or NULL;
  *   ws >= qlora_workspace_size(QLORA_OP_ACT_BWD, W, M, r, 0).
@@ -467,7 +468,7 @@ QLORA_API qlora_status_t qlora_debug_decode_rate(int fmt, int iters,
  * "stream_fwd", "stream_dx", "stream_reduce" (batches of 65-256 rows), "short_fwd", "short_dx"
  * (batches of up to 64 rows), "w4a8_quant", "w4a8_gemm", "norm_fwd", "norm_bwd", "norm_dgamma",
  * "gated_fwd", "gated_dx", "act_fwd", "act_down" (gradients behind an activation), "bias_sum",
- * "narrow_down_T" (batches of up to 16 rows), "split_sum".
+ * "narrow_down_T" (batches of up to 64 rows), "split_sum", "down_sum".
  * Host-side bookkeeping only; the compute path is unchanged when profiling is off. */
 QLORA_API int64_t qlora_launch_count(void);
 QLORA_API qlora_status_t qlora_profile_enable(int enable);
