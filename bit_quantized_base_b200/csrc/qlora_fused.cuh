@@ -63,6 +63,9 @@
 //   Both (and kEpiAct's dX, which is the plain one otherwise) can split a tile's contraction over S
 //   work items, for batches whose tiles leave most CTA pairs idle: each item stores its fp32
 //   accumulator and qlora_split_kernel adds them in order and runs the epilogue.
+//   RB = 1 (at most 256 rows): one MMA block per tile; the room its second activation block leaves
+//   goes to a code ring of 16 stages, and scales are loaded four own steps ahead.  A step then takes
+//   half the tensor time, and with 4 code stages the memory's latency, not the decode, set the pace.
 #pragma once
 #include <cuda_bf16.h>
 #include "qlora_ptx.cuh"
@@ -84,13 +87,16 @@ constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kCodeWarp = 6, kDqWarp0
 constexpr int kThreads = (kDqWarp0 + kDqWarps) * 32;
 constexpr int kTmemCols = 512;         // 2 blocks x 256 columns
 constexpr int GM = 8;                  // m-tiles per raster group
-constexpr int kNumBars = 2 * NS + 2 * NC + 2;
 // epilogue staging: per epilogue warp one tile of 32 rows x 32 output columns (bf16)
 constexpr int STG_BYTES = 32 * 32 * 2;
-constexpr size_t kStgOff = size_t(NS) * (MB * X_BYTES + W_BYTES) + size_t(NC) * C_BYTES + 1024;
-constexpr size_t kSmemBase = 1024 + kStgOff + size_t(kEpiWarps) * STG_BYTES;
+// rb: MMA blocks of 256 rows per tile (2, or 1 in the kernels for at most 256 rows)
+__host__ __device__ constexpr int code_stages(int rb) { return rb == 1 ? 16 : NC; }
+__host__ __device__ constexpr size_t stg_off(int rb) {
+  return size_t(NS) * (rb * X_BYTES + W_BYTES) + size_t(code_stages(rb)) * C_BYTES + 1024;
+}
+__host__ __device__ constexpr size_t smem_base(int rb) { return 1024 + stg_off(rb) + size_t(kEpiWarps) * STG_BYTES; }
 // plus the expert table: 2 x (E + 1) ints
-__host__ __device__ constexpr size_t smem_bytes(int E) { return kSmemBase + size_t(2) * (E + 1) * 4; }
+__host__ __device__ constexpr size_t smem_bytes(int E, int rb = MB) { return smem_base(rb) + size_t(2) * (E + 1) * 4; }
 }  // namespace fused
 
 struct FusedParams {
@@ -262,11 +268,12 @@ struct ItemGeom {
   }
 };
 
-template <int FMT, bool DX, int EPI = kEpiPlain, bool SPLIT = false>
+template <int FMT, bool DX, int EPI = kEpiPlain, bool SPLIT = false, int RB = fused::MB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fused::kThreads, 1)
 qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::type p) {
   using namespace fused;
   constexpr bool EX = EPI != kEpiPlain;
+  constexpr int MB = RB, NC = code_stages(RB), kNumBars = 2 * NS + 2 * NC + 2;
   constexpr bool GATED = EPI == kEpiGated;
   constexpr bool DUAL = GATED && DX;           // contraction over both weights' rows
   constexpr int TN = GATED && !DX ? HN : BN;   // output columns of a tile
@@ -280,7 +287,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* pair_slot = tmem_slot + 2;
-  int* s_off = reinterpret_cast<int*>(smem + (kSmemBase - 1024));
+  int* s_off = reinterpret_cast<int*>(smem + (smem_base(RB) - 1024));
   int* s_first = s_off + (p.E + 1);
 
   const uint32_t b0 = ptx::smem_u32(bars);
@@ -362,7 +369,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
     }
     PairTile pt = pair_tile_at<DX>(grp_view, t, p.num_n, p.tail_split);
     if constexpr (EX) {
-      if (pt.row0 + 2 * HM >= pt.row_end) pt.nb = 1;   // no rows in the second block
+      if (RB == 1 || pt.row0 + 2 * HM >= pt.row_end) pt.nb = 1;   // no rows in the second block
     }
     return pt;
   };
@@ -463,7 +470,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
           const uint64_t a = a0 + st * kAStage, b = b0d + st * kBStage;
           if (ks < nk) {
             const uint32_t acc0 = ks > kb ? 1u : 0u;
-            if (nb == 2) {
+            if (RB == 2 && nb == 2) {
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk) {
                 ptx::mma_bf16_pair(tmem, a + kk * kAkk, b + kk * kBkk, idesc, kk ? 1u : acc0);
@@ -479,7 +486,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
             const uint32_t acc0 = SPLIT && ks == kb ? 0u : 1u;     // a split range may hold LoRA steps only
             for (int kk = 0; kk < kks; ++kk) {
               ptx::mma_bf16_pair(tmem, a + kk * kAkk, b + kk * kBkk, idesc, kk ? 1u : acc0);
-              if (nb == 2) ptx::mma_bf16_pair(tmem + BN, a + kABlk + kk * kAkk, b + kk * kBkk, idesc, kk ? 1u : acc0);
+              if (RB == 2 && nb == 2) ptx::mma_bf16_pair(tmem + BN, a + kABlk + kk * kAkk, b + kk * kBkk, idesc, kk ? 1u : acc0);
             }
           }
           ptx::mma_commit_pair(empty_s(st), 3);
@@ -513,7 +520,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
     const int q = warp;  // tensor-memory lanes 32q .. 32q+31
     const int ncols = DX ? p.K : p.N;
     const uint32_t acc_empty_leader = ptx::mapa(acc_empty, 0);
-    const uint32_t stg = ptx::smem_u32(smem + kStgOff) + uint32_t(q) * STG_BYTES;
+    const uint32_t stg = ptx::smem_u32(smem + stg_off(RB)) + uint32_t(q) * STG_BYTES;
     const uint32_t wsw = (uint32_t(lane) >> 1) & 3u;             // write swizzle of row `lane`
     const int rr0 = lane >> 2, rc = lane & 3;                     // read: row rr0 + 8 it, chunk rc
     uint32_t tc = 0;
@@ -701,12 +708,18 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
     Cursor cur{pair, 0, 0, 0, 0, 0, 0u, 0u};
     set_item(cur, 0);
     advance(cur, grp);
+    // scales of this step and the next AHEAD own steps
+    constexpr int AHEAD = RB == 1 ? 4 : 2;
     Cursor pf = cur;
-    advance(pf, 2);
-    ItemScale s_cur = scale_for(cur), s_next = scale_for(pf);
-    advance(pf, 2);
+    ItemScale sc_q[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      sc_q[k] = scale_for(pf);
+      advance(pf, 2);
+    }
     while (cur.t < num_items) {
-      const ItemScale s_pref = scale_for(pf);   // two own steps ahead
+      const ItemScale s_pref = scale_for(pf);   // AHEAD own steps ahead
+      const ItemScale s_cur = sc_q[0];
       advance(pf, 2);
       const uint32_t i = cur.i;                                    // pipeline step
       const uint32_t sw = i % NS, pw = (i / NS) & 1u;
@@ -782,8 +795,9 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(full_s(sw));
-      s_cur = s_next;
-      s_next = s_pref;
+#pragma unroll
+      for (int k = 0; k + 1 < AHEAD; ++k) sc_q[k] = sc_q[k + 1];
+      sc_q[AHEAD - 1] = s_pref;
       advance(cur, 2);
     }
   }

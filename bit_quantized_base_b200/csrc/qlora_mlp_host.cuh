@@ -11,12 +11,12 @@ const float* ts_of(const qlora_weight_t* W) {
 
 bool act_valid(int act) { return act >= QLORA_ACT_NONE && act <= QLORA_ACT_GELU_TANH; }
 
-template <int FMT, bool DX, int EPI, bool SPLIT>
+template <int FMT, bool DX, int EPI, bool SPLIT, int RB>
 qlora_status_t launch_fused_ex_s(const FusedExParams& p, int grid, bool early, cudaStream_t st) {
-  const size_t smem = fused::smem_bytes(1);
-  if (!set_smem(qlora_fused_gemm_kernel<FMT, DX, EPI, SPLIT>, smem)) return QLORA_ERR_CUDA;
+  const size_t smem = fused::smem_bytes(1, RB);
+  if (!set_smem(qlora_fused_gemm_kernel<FMT, DX, EPI, SPLIT, RB>, smem)) return QLORA_ERR_CUDA;
   LaunchScope scope(EPI == kEpiAct ? (DX ? kKindFusedDx : kKindActFwd) : (DX ? kKindGatedDx : kKindGatedFwd), st);
-  if (launch_pdl(qlora_fused_gemm_kernel<FMT, DX, EPI, SPLIT>, dim3(grid), dim3(fused::kThreads), smem, st, p,
+  if (launch_pdl(qlora_fused_gemm_kernel<FMT, DX, EPI, SPLIT, RB>, dim3(grid), dim3(fused::kThreads), smem, st, p,
                  early) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
@@ -24,8 +24,9 @@ qlora_status_t launch_fused_ex_s(const FusedExParams& p, int grid, bool early, c
 
 template <int FMT, bool DX, int EPI>
 qlora_status_t launch_fused_ex_t(const FusedExParams& p, int grid, bool early, cudaStream_t st) {
-  return p.splits > 1 ? launch_fused_ex_s<FMT, DX, EPI, true>(p, grid, early, st)
-                      : launch_fused_ex_s<FMT, DX, EPI, false>(p, grid, early, st);
+  if (p.splits == 1) return launch_fused_ex_s<FMT, DX, EPI, false, 2>(p, grid, early, st);
+  return p.M <= 2 * fused::HM ? launch_fused_ex_s<FMT, DX, EPI, true, 1>(p, grid, early, st)
+                              : launch_fused_ex_s<FMT, DX, EPI, true, 2>(p, grid, early, st);
 }
 
 // early: the launch may start beside the kernel before it (which must then not write this
@@ -189,10 +190,16 @@ qlora_status_t launch_act_down(int nb, int act, const void* dy, const void* a0, 
   return QLORA_OK;
 }
 
+// Up to this many rows the adapter gradients run ahead of dX on the same stream: a few microseconds,
+// after which dX may be launched early (its predecessor has waited for the gradients it reads), and
+// no events.  Longer batches run them beside dX.  Measured: gated, 77 rows of 2048 x 512, 44 us ahead
+// and 48 beside; 1021 rows of 8192 x 2048, 87 ahead and 82 beside.
+constexpr int64_t kWgradFirstRows = 256;
+
 // Runs `side_work` on the device's side stream beside `main_work` on `s`, joined into `s` again.  The
-// first kernel of main_work reads what act_down, the last kernel on `s`, writes, so it is launched
-// without the permission to start early; launched early, it would also hold back the fork event and
-// with it side_work, until its own end (measured).
+// first kernel of main_work reads what the kernels before on `s` have only just written, so it is
+// launched without the permission to start early; launched early, it would also hold back the fork
+// event and with it side_work, until its own end (measured).
 template <class F, class G>
 qlora_status_t fork_join(cudaStream_t s, F&& side_work, G&& main_work) {
   SideStream* side = side_stream();
@@ -218,9 +225,9 @@ template <int NB>
 qlora_status_t launch_narrow_down_t(const NarrowDownParams& p, unsigned groups, cudaStream_t st) {
   if (!set_smem(qlora_narrow_down_kernel<NB>, 0)) return QLORA_ERR_CUDA;
   LaunchScope scope(kKindNarrowDown, st);
-  if (launch_pdl_cluster(qlora_narrow_down_kernel<NB>, dim3(groups * unsigned(p.S)),
-                         dim3(narrow::kDownWarps * 32), 0,
-                         st, p, unsigned(p.S)) != cudaSuccess)
+  const dim3 grid(groups * unsigned(p.S), unsigned((p.M + 8 * NB - 1) / (8 * NB)));
+  if (launch_pdl_cluster(qlora_narrow_down_kernel<NB>, grid, dim3(narrow::kDownWarps * 32), 0, st, p,
+                         unsigned(p.S)) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
@@ -252,7 +259,7 @@ NarrowWeight narrow_weight(const qlora_weight_t* W, const void* B) {
 }
 
 // Blocks of 8 batch rows, as the kernels are compiled for.
-int narrow_blocks(int64_t M) { return M <= 8 ? 1 : (M <= 16 ? 2 : (M <= 32 ? 4 : 8)); }
+int narrow_blocks(int64_t M) { return M <= 8 ? 1 : 2; }
 
 // T [nw][M, r] and Zs [M, nw r] of one or two adapters (Wu, Au null: one).
 qlora_status_t narrow_down(const qlora_weight_t* Wg, const qlora_weight_t* Wu, const void* X, const void* Ag,
@@ -272,16 +279,10 @@ qlora_status_t narrow_down(const qlora_weight_t* Wg, const qlora_weight_t* Wu, c
   d.r = r;
   d.nw = nw;
   d.ldzs = nw * r;
-  d.S = K >= 8192 ? 8 : (K >= 2048 ? 4 : 1);
+  d.S = K >= 4096 ? 8 : (K >= 1024 ? 4 : 1);
   d.s = scale;
-  d.zs_mul = 1.0f;
   const unsigned groups = unsigned((nw * r + 15) / 16);
-  switch (nb) {
-    case 1: return launch_narrow_down_t<1>(d, groups, st);
-    case 2: return launch_narrow_down_t<2>(d, groups, st);
-    case 4: return launch_narrow_down_t<4>(d, groups, st);
-    default: return launch_narrow_down_t<8>(d, groups, st);
-  }
+  return nb == 1 ? launch_narrow_down_t<1>(d, groups, st) : launch_narrow_down_t<2>(d, groups, st);
 }
 
 // T and Zs by the kernels of the batch size: in the forward, and in a backward call that was not
@@ -449,7 +450,9 @@ qlora_status_t qlora_gated_mlp_bwd(const qlora_weight_t* Wg, const qlora_weight_
                         &up);
   };
   if (!dX) return wgrads(s);
-  return fork_join(s, wgrads, [&]() {
+  const bool beside = M > kWgradFirstRows;
+  if (!beside && (st = wgrads(s)) != QLORA_OK) return st;
+  auto run_dx = [&]() {
     FusedExParams p{};
     int grid = 0;
     const SplitPlan sp = split_dx(N, K, M, r, 2, num_sms(), ws_bytes - L.partial);
@@ -463,9 +466,10 @@ qlora_status_t qlora_gated_mlp_bwd(const qlora_weight_t* Wg, const qlora_weight_
     p.scales_up = Wu->scales;
     p.scales2_up = Wu->scales2;
     p.lora_up_up = static_cast<const __nv_bfloat16*>(Au);
-    e = launch_fused_ex<true, kEpiGated>(Wg->fmt, p, grid, false, s);
+    e = launch_fused_ex<true, kEpiGated>(Wg->fmt, p, grid, !beside, s);
     return e != QLORA_OK || sp.S == 1 ? e : launch_split(p, p.K, false, s);
-  });
+  };
+  return beside ? fork_join(s, wgrads, run_dx) : run_dx();
 }
 
 qlora_status_t qlora_linear_act_fwd(const qlora_weight_t* W, const void* X, const void* A, const void* B,
@@ -564,8 +568,9 @@ qlora_status_t qlora_linear_act_bwd(const qlora_weight_t* W, const void* X, cons
     return QLORA_OK;
   };
   if (!dX) return side_work(s);
-  return fork_join(s, side_work, [&]() {
-    const bool early = grad[0] == nullptr;   // else dZ is act_down's
+  const bool early = M <= kWgradFirstRows;
+  if (early && (st = side_work(s)) != QLORA_OK) return st;
+  auto run_dx = [&]() {
     if (short_dx) return launch_short(W, true, dZ, w + L.zs, A, dX, M, r, ws, part, region, s, early);
     if (stream_dx)
       return launch_stream(W, true, dZ, w + L.zs, A, dX, M, r, ws_status(ws), part, region, s, early);
@@ -576,7 +581,8 @@ qlora_status_t qlora_linear_act_bwd(const qlora_weight_t* W, const void* X, cons
     if (e != QLORA_OK) return e;
     e = launch_fused_ex<true, kEpiAct>(W->fmt, p, grid, early, s);
     return e != QLORA_OK || sp.S == 1 ? e : launch_split(p, p.K, false, s);
-  });
+  };
+  return early ? run_dx() : fork_join(s, side_work, run_dx);
 }
 
 }  // extern "C"

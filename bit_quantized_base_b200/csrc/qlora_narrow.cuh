@@ -551,14 +551,14 @@ qlora_narrow_kernel(const __grid_constant__ NarrowParams p) {
 }
 
 // T = X A^T and Zs for nw adapters of rank r: the 16-row operand is 16 rows of the adapters stacked
-// (row j < r: A0, else A1), the 8-wide one the batch rows.  8 warps split the depth of a CTA, S CTAs of
-// a cluster that of a row group; the sums meet in shared memory in warp and rank order.
+// (row j < r: A0, else A1), the 8-wide one the batch rows (blockIdx.y: a block of 8 NB of them).  8
+// warps split the depth of a CTA, S CTAs of a cluster that of a row group; the sums meet in shared memory in warp and rank order.
 struct NarrowDownParams {
   const __nv_bfloat16 *a0, *a1, *x;   // [r, K] each (a1 null: one adapter); [M, K]
   const float *ts0, *ts1;             // tensor scales, or null
   __nv_bfloat16 *t, *zs;              // [nw][M, r]; [M, ldzs]
   int M, K, r, nw, ldzs, S;
-  float s, zs_mul;
+  float s;
 };
 
 template <int NB>
@@ -571,6 +571,7 @@ qlora_narrow_down_kernel(const __grid_constant__ NarrowDownParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rank = int(blockIdx.x) % p.S, grp = int(blockIdx.x) / p.S;
+  const int m0 = int(blockIdx.y) * NB * 8, mrows = min(NB * 8, p.M - m0);
   const int rows = p.nw * p.r;
   const __nv_bfloat16* ar[2];
 #pragma unroll
@@ -592,7 +593,7 @@ qlora_narrow_down_kernel(const __grid_constant__ NarrowDownParams p) {
     const uint4 a = __ldg(reinterpret_cast<const uint4*>(ar[0] + k)), c = __ldg(reinterpret_cast<const uint4*>(ar[1] + k));
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int m = 8 * b + g;
+      const int m = m0 + 8 * b + g;
       const uint4 x = m < p.M ? __ldg(reinterpret_cast<const uint4*>(p.x + size_t(m) * p.K + k)) : zero;
       mma16816(acc[b], a.x, c.x, a.y, c.y, x.x, x.y);
       mma16816(acc[b], a.z, c.z, a.w, c.w, x.z, x.w);
@@ -615,7 +616,7 @@ qlora_narrow_down_kernel(const __grid_constant__ NarrowDownParams p) {
   if (p.S > 1) ptx::cluster_sync();
   else __syncthreads();
   if (rank == 0) {
-    for (int e = int(threadIdx.x); e < 16 * p.M; e += kDownWarps * 32) {
+    for (int e = int(threadIdx.x); e < 16 * mrows; e += kDownWarps * 32) {
       const int jj = e % 16, m = e / 16, j = grp * 16 + jj;
       if (j >= rows) continue;
       float v = 0.0f;
@@ -627,9 +628,9 @@ qlora_narrow_down_kernel(const __grid_constant__ NarrowDownParams p) {
       }
       const int i = j >= p.r ? 1 : 0;
       const float* ts = i ? p.ts1 : p.ts0;
-      const float zs = p.s / (ts ? __ldg(ts) : 1.0f) * p.zs_mul;
-      p.t[(size_t(i) * p.M + m) * p.r + (j - i * p.r)] = __float2bfloat16_rn(v);
-      p.zs[size_t(m) * p.ldzs + j] = __float2bfloat16_rn(v * zs);
+      const float zs = p.s / (ts ? __ldg(ts) : 1.0f);
+      p.t[(size_t(i) * p.M + m0 + m) * p.r + (j - i * p.r)] = __float2bfloat16_rn(v);
+      p.zs[size_t(m0 + m) * p.ldzs + j] = __float2bfloat16_rn(v * zs);
     }
   }
   if (p.S > 1) ptx::cluster_sync();          // every rank's sums stay until they are read
