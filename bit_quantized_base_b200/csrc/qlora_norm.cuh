@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(T) qlora_norm_bwd_kernel(const __grid_constant
     } else {
       float lo;
       rstd_pair(double(group_sum(sq, p.G, red2)) * double(inv_k) + double(p.eps), rstd, lo);
+      if (!live) rstd = 0.0f;                  // no row: with eps = 0 it would be infinite, and 0 rstd NaN
     }
     const float c = dot * inv_k * rstd * rstd;
 #pragma unroll

@@ -273,3 +273,20 @@ def test_w4a8_takes_the_norm_s_codes():
     torch.cuda.synchronize()
     assert Q.qlora_get_device_status(ws) == 0
     assert torch.equal(out[0], out[1]) and torch.equal(T[0], T[1])
+
+
+@pytest.mark.parametrize("M,K", [(1, 512), (3, 96), (600, 40), (593, 4096)])
+def test_gain_gradient_without_epsilon_and_rstd(M, K):
+    """eps = 0 with rstd recomputed: the row slots behind the last row add nothing to dgamma."""
+    from bit_quantized_base_b200 import qlora as Q
+    rng = np.random.default_rng(M + K)
+    S, dY = bf16(rng, (M, K)), bf16(rng, (M, K))
+    g = bf16(rng, (K,))
+    dS, dg = torch.empty(M, K, dtype=BF, device="cuda"), torch.empty(K, dtype=BF, device="cuda")
+    ws = torch.zeros(Q.qlora_rmsnorm_workspace_size(M, K), dtype=torch.uint8, device="cuda")
+    Q.qlora_rmsnorm_bwd(S.cuda(), None, g.cuda(), 0.0, dY.cuda(), None, dS, dg, M, K, ws)
+    torch.cuda.synchronize()
+    rstd = 1.0 / np.sqrt((f64(S) ** 2).mean(axis=1))
+    terms = f64(dY) * f64(S) * rstd[:, None]
+    # binary32 sums of at most M terms, each with a few roundings of its own
+    close(dg, terms.sum(axis=0), (M + 16) * 2.0 ** -24 * np.abs(terms).sum(axis=0), "dgamma")
