@@ -64,6 +64,12 @@ __device__ __forceinline__ void rstd_pair(double ms, float& hi, float& lo) {
   }
 }
 
+// Whether a product's binary32 estimate (at most 3 units of its last place off: two roundings and
+// rstd's) lies so near the border of two bf16 values that they could decide: its low 16 bits within 8
+// of the middle.  Returned as a value to take the minimum of: at most kNearBorder if so.
+constexpr uint32_t kNearBorder = 16u << 16;
+__device__ __forceinline__ uint32_t border(float y) { return (__float_as_uint(y) << 16) + (0x8008u << 16); }
+
 // bf16(s rstd gamma) as if computed exactly, up to about 2^-44 of the value: the two products'
 // rounding errors are carried (fused multiply-adds return them exactly), and a binary32 sum that
 // lands on the border between two bf16 values goes to the side its error points to.  An 8-bit
@@ -132,25 +138,26 @@ __global__ void __launch_bounds__(T) qlora_norm_fwd_kernel(const __grid_constant
       if (p.s && live && v < nv) st_v4(p.s + base + size_t(v) * 8, s[j]);
     }
   }
-  // at most 32 squares (exact in binary32) per thread in binary32 (MX: with the rounding
+  // at most 32 squares (exact in binary32) per thread in two binary32 sums (MX: with the rounding
   // error of every addition, which a two-sum returns exactly, summed beside), then binary64
-  float sq = 0.0f, comp = 0.0f;
+  float2 sq = make_float2(0.0f, 0.0f), comp = sq;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const uint32_t a[4] = {s[j].x, s[j].y, s[j].z, s[j].w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float f = (i & 1) ? hi_f32(a[i >> 1]) : lo_f32(a[i >> 1]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = make_float2(lo_f32(a[i]), hi_f32(a[i]));
       if constexpr (MX) {
-        const float q = __fmul_rn(f, f), n = __fadd_rn(sq, q), b = __fadd_rn(n, -sq);
-        comp = __fadd_rn(comp, __fadd_rn(__fadd_rn(sq, -__fadd_rn(n, -b)), __fadd_rn(q, -b)));
+        const float2 q = ptx::mul2(f, f), n = ptx::add2(sq, q), b = ptx::sub2(n, sq);
+        comp = ptx::add2(comp, ptx::add2(ptx::sub2(sq, ptx::sub2(n, b)), ptx::sub2(q, b)));
         sq = n;
       } else {
-        sq = fmaf(f, f, sq);
+        sq.x = fmaf(f.x, f.x, sq.x);
+        sq.y = fmaf(f.y, f.y, sq.y);
       }
     }
   }
-  const double sum = group_sum(double(sq) + double(comp), p.G, red);
+  const double sum = group_sum((double(sq.x) + double(sq.y)) + (double(comp.x) + double(comp.y)), p.G, red);
   float hi, lo;
   rstd_pair(sum / double(p.K) + double(p.eps), hi, lo);
   if (p.rstd && live && t == 0) p.rstd[row] = hi;
@@ -162,28 +169,43 @@ __global__ void __launch_bounds__(T) qlora_norm_fwd_kernel(const __grid_constant
     uint4 gv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
     if (p.gamma && ok) gv = __ldg(reinterpret_cast<const uint4*>(p.gamma) + v);
     const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w};
-    uint32_t o[4];
+    uint32_t o[4], near = 0xFFFFFFFFu;
+    [[maybe_unused]] uint2 e[4];               // MX: how near a border each product is
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (MX)
-        o[i] = product_bf16(lo_f32(a[i]), hi, lo, lo_f32(g[i])) |
-               (product_bf16(hi_f32(a[i]), hi, lo, hi_f32(g[i])) << 16);
-      else
-        o[i] = ptx::cvt_bf16x2(lo_f32(a[i]) * hi * lo_f32(g[i]), hi_f32(a[i]) * hi * hi_f32(g[i]));
+      const float2 y = ptx::mul2(ptx::mul2(make_float2(lo_f32(a[i]), hi_f32(a[i])), make_float2(hi, hi)),
+                                 make_float2(lo_f32(g[i]), hi_f32(g[i])));
+      o[i] = ptx::cvt_bf16x2(y.x, y.y);
+      if constexpr (MX) {
+        e[i] = make_uint2(border(y.x), border(y.y));
+        near = min(near, min(e[i].x, e[i].y));
+      }
+    }
+    if constexpr (MX) {
+      if (near <= kNearBorder) {               // about one element in 4000
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (e[i].x <= kNearBorder)
+            o[i] = (o[i] & 0xFFFF0000u) | product_bf16(lo_f32(a[i]), hi, lo, lo_f32(g[i]));
+          if (e[i].y <= kNearBorder)
+            o[i] = (o[i] & 0xFFFFu) | (product_bf16(hi_f32(a[i]), hi, lo, hi_f32(g[i])) << 16);
+        }
+      }
     }
     if (p.y && ok) st_v4(p.y + base + size_t(v) * 8, make_uint4(o[0], o[1], o[2], o[3]));
     if constexpr (MX) {
       uint32_t amax = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) amax = max(amax, max(o[i] & 0x7FFFu, (o[i] >> 16) & 0x7FFFu));
+      for (int i = 0; i < 4; ++i) amax = __vmaxu2(amax, o[i] & 0x7FFF7FFFu);
+      amax = max(amax & 0xFFFFu, amax >> 16);
       amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      const int e = mxfp8_exponent(amax);
-      const float inv = mxfp8_inverse(e);
+      const int ex = mxfp8_exponent(amax);
+      const float inv = mxfp8_inverse(ex);
       if (ok) {
         const uint2 c = make_uint2(mxfp8_encode4(o[0], o[1], inv), mxfp8_encode4(o[2], o[3], inv));
         *reinterpret_cast<uint2*>(p.codes + base + size_t(v) * 8) = c;
-        if ((v & 3) == 0) p.scales[(base + size_t(v) * 8) / 32] = uint8_t(e);
+        if ((v & 3) == 0) p.scales[(base + size_t(v) * 8) / 32] = uint8_t(ex);
       }
     }
   }
@@ -199,52 +221,99 @@ struct NormBwdParams {
   float eps;
 };
 
-// Persistent over rows: group g of the grid takes rows g, g + groups, ...  With DG each thread
-// keeps its columns' dgamma sums in registers over all its rows; the CTA's groups add theirs in
-// group order through shared memory and write one partial row, which qlora_norm_dgamma_kernel sums.
+// CTAs per SM and, per CTA, the rows a group keeps in flight or in shared memory.
+namespace norm {
+__host__ __device__ constexpr int bwd_per_sm(int T) { return T > 512 ? 1 : (T > 256 ? 2 : 3); }
+__host__ __device__ constexpr size_t bwd_stage_bytes(int V, int T) { return size_t(3) * V * T * 16; }
+__host__ __device__ constexpr int bwd_stages(int V, int T) {
+  const int n = int(size_t(225) * 1024 / bwd_per_sm(T) / bwd_stage_bytes(V, T));
+  return n < 1 ? 1 : (n > 4 ? 4 : n);
+}
+}  // namespace norm
+
+// Persistent over rows: group g of the grid takes rows g, g + groups, ...  Every thread copies the
+// vectors of S, dY and dS_in that it will work on into its own slots of a ring in shared memory,
+// up to four rows ahead (asynchronously, so no registers hold them and no barrier guards them: the
+// slots are the thread's own).  With DG each thread keeps its columns' dgamma sums in registers over
+// all its rows; the CTA's groups add theirs in group order through shared memory and write one
+// partial row, which qlora_norm_dgamma_kernel sums.
 template <int V, bool DG, int T>
-__global__ void __launch_bounds__(T) qlora_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+__global__ void __launch_bounds__(T, norm::bwd_per_sm(T)) qlora_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
   using namespace norm;
+  constexpr int S = bwd_stages(V, T);
   __shared__ float red[32], red2[32];
-  extern __shared__ float gsum[];              // DG, several groups: [groups - 1][K]
+  extern __shared__ __align__(16) uint8_t ring[];   // [S][S, dY, dS_in][V][T] vectors
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int groups = int(blockDim.x) / p.G;
+  const int groups = T / p.G;
   const int grp = int(threadIdx.x) / p.G;
   const int t = int(threadIdx.x) & (p.G - 1);
   const int nv = p.K / 8;
   const float inv_k = 1.0f / float(p.K);
+  const uint4 one4 = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  // gamma stays in registers, but for 3 and 4 vectors a thread, which have none left
+  auto load_gamma = [&](int j) {
+    const int v = j * p.G + t;
+    return p.gamma && v < nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma) + v) : one4;
+  };
+  uint4 gam[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) gam[j] = V <= 2 ? load_gamma(j) : one4;
   float acc[DG ? V * 8 : 1];
 #pragma unroll
   for (int i = 0; i < (DG ? V * 8 : 1); ++i) acc[i] = 0.0f;
-  for (long long r0 = (long long)blockIdx.x * groups; r0 < p.M; r0 += (long long)gridDim.x * groups) {
-    const long long row = r0 + grp;
+  const uint4* slots = reinterpret_cast<const uint4*>(ring) + threadIdx.x;
+  const uint32_t slot0 = ptx::smem_u32(slots);
+  const long long step = (long long)gridDim.x * groups;
+  // one row's vectors into stage sg; past the last row or the row's end: zeros
+  auto fetch = [&](long long row, int sg) {
     const bool live = row < p.M;
     const size_t base = size_t(live ? row : 0) * size_t(p.K);
-    uint4 s[V], d[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = j * p.G + t;
-      s[j] = d[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && v < nv) {
-        s[j] = ld_v4(p.s + base + size_t(v) * 8);
-        d[j] = ld_v4(p.dy + base + size_t(v) * 8);
-      }
+      const uint32_t bytes = live && v < nv ? 16u : 0u;
+      const size_t at = base + size_t(v < nv ? v : 0) * 8;
+      const uint32_t dst = slot0 + uint32_t((sg * 3 * V + j) * T) * 16u;
+      ptx::cp_async_16(dst, p.s + at, bytes);
+      ptx::cp_async_16(dst + uint32_t(V * T) * 16u, p.dy + at, bytes);
+      if (p.ds_in) ptx::cp_async_16(dst + uint32_t(2 * V * T) * 16u, p.ds_in + at, bytes);
     }
+  };
+  long long row = (long long)blockIdx.x * groups + grp;
+  // the CTA's groups run the same number of rows (the last may be past the end)
+  const long long first = (long long)blockIdx.x * groups;
+  const int count = first < p.M ? int((p.M - first + step - 1) / step) : 0;
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) {
+    fetch(row + i * step, i);
+    ptx::cp_async_commit();
+  }
+  int sg = 0, pf = S - 1;
+  for (int it = 0; it < count; ++it, row += step) {
+    fetch(row + (S - 1) * step, pf);
+    ptx::cp_async_commit();
+    ptx::cp_async_wait<S - 1>();
+    const bool live = row < p.M;
+    const size_t base = size_t(live ? row : 0) * size_t(p.K);
+    const uint4* my = slots + sg * 3 * V * T;
+    pf = sg;
+    sg = sg + 1 == S ? 0 : sg + 1;
     float dot = 0.0f, sq = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int v = j * p.G + t;
-      const uint32_t a[4] = {s[j].x, s[j].y, s[j].z, s[j].w}, b[4] = {d[j].x, d[j].y, d[j].z, d[j].w};
-      uint4 gv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-      if (p.gamma && v < nv) gv = __ldg(reinterpret_cast<const uint4*>(p.gamma) + v);
+      const uint4 sv = my[j * T], dv = my[(V + j) * T];
+      const uint32_t a[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {dv.x, dv.y, dv.z, dv.w};
+      const uint4 gv = V <= 2 ? gam[j] : load_gamma(j);
       const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         dot = fmaf(lo_f32(b[i]) * lo_f32(g[i]), lo_f32(a[i]), dot);
         dot = fmaf(hi_f32(b[i]) * hi_f32(g[i]), hi_f32(a[i]), dot);
-        sq = fmaf(lo_f32(a[i]), lo_f32(a[i]), sq);
-        sq = fmaf(hi_f32(a[i]), hi_f32(a[i]), sq);
+        if (!p.rstd) {
+          sq = fmaf(lo_f32(a[i]), lo_f32(a[i]), sq);
+          sq = fmaf(hi_f32(a[i]), hi_f32(a[i]), sq);
+        }
       }
     }
     dot = group_sum(dot, p.G, red);
@@ -260,13 +329,12 @@ __global__ void __launch_bounds__(T) qlora_norm_bwd_kernel(const __grid_constant
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = j * p.G + t;
-      const bool ok = live && v < nv;
-      const uint32_t a[4] = {s[j].x, s[j].y, s[j].z, s[j].w}, b[4] = {d[j].x, d[j].y, d[j].z, d[j].w};
-      uint4 gv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-      if (p.gamma && ok) gv = __ldg(reinterpret_cast<const uint4*>(p.gamma) + v);
+      const uint4 sv = my[j * T], dv = my[(V + j) * T];
+      const uint32_t a[4] = {sv.x, sv.y, sv.z, sv.w}, b[4] = {dv.x, dv.y, dv.z, dv.w};
+      const uint4 gv = V <= 2 ? gam[j] : load_gamma(j);
       const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w};
       uint4 iv = make_uint4(0u, 0u, 0u, 0u);
-      if (p.ds_in && ok) iv = ld_v4(p.ds_in + base + size_t(v) * 8);
+      if (p.ds_in) iv = my[(2 * V + j) * T];
       const uint32_t in[4] = {iv.x, iv.y, iv.z, iv.w};
       uint32_t o[4];
 #pragma unroll
@@ -280,11 +348,14 @@ __global__ void __launch_bounds__(T) qlora_norm_bwd_kernel(const __grid_constant
           acc[j * 8 + 2 * i + 1] = fmaf(d1, s1 * rstd, acc[j * 8 + 2 * i + 1]);
         }
       }
-      if (ok) st_v4(p.ds + base + size_t(v) * 8, make_uint4(o[0], o[1], o[2], o[3]));
+      if (live && v < nv) st_v4(p.ds + base + size_t(v) * 8, make_uint4(o[0], o[1], o[2], o[3]));
     }
   }
   if constexpr (DG) {
+    float* gsum = reinterpret_cast<float*>(ring);   // [groups - 1][K]
     if (groups > 1) {
+      ptx::cp_async_wait<0>();
+      __syncthreads();                         // the ring is every thread's from here
       if (grp > 0) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {

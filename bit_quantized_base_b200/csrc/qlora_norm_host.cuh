@@ -27,46 +27,57 @@ NormPlan norm_plan(int64_t K, int want) {
 // The backward kernel holds two rows and the dgamma sums, so it stops at two.
 int norm_vectors(int64_t M, int sms, bool bwd) { return M <= 4 * int64_t(sms) ? 1 : (bwd ? 2 : 4); }
 
-template <bool MX, int T>
-cudaError_t launch_norm_fwd_t(int V, unsigned grid, const NormFwdParams& p, cudaStream_t st) {
-  switch (V) {
-    case 1: return launch_pdl(qlora_norm_fwd_kernel<1, MX, T>, dim3(grid), dim3(T), 0, st, p);
-    case 2: return launch_pdl(qlora_norm_fwd_kernel<2, MX, T>, dim3(grid), dim3(T), 0, st, p);
-    case 3: return launch_pdl(qlora_norm_fwd_kernel<3, MX, T>, dim3(grid), dim3(T), 0, st, p);
-    default: return launch_pdl(qlora_norm_fwd_kernel<4, MX, T>, dim3(grid), dim3(T), 0, st, p);
-  }
+// The (V, T) that norm_plan makes: more than two vectors a thread only in groups of more than want = 4
+// (forward) or 2 (backward) leaves, 512 threads with two only in the backward pass.
+template <bool MX, int V, int T>
+cudaError_t launch_norm_fwd_t(unsigned grid, const NormFwdParams& p, cudaStream_t st) {
+  return launch_pdl(qlora_norm_fwd_kernel<V, MX, T>, dim3(grid), dim3(T), 0, st, p);
 }
 
 template <bool MX>
 cudaError_t launch_norm_fwd(const NormPlan& np, unsigned grid, const NormFwdParams& p, cudaStream_t st) {
-  if (np.threads == 256) return launch_norm_fwd_t<MX, 256>(np.V, grid, p, st);
-  if (np.threads == 512) return launch_norm_fwd_t<MX, 512>(np.V, grid, p, st);
-  return launch_norm_fwd_t<MX, 1024>(np.V, grid, p, st);
+  switch (np.threads * 8 + np.V) {
+    case 256 * 8 + 1: return launch_norm_fwd_t<MX, 1, 256>(grid, p, st);
+    case 256 * 8 + 2: return launch_norm_fwd_t<MX, 2, 256>(grid, p, st);
+    case 256 * 8 + 3: return launch_norm_fwd_t<MX, 3, 256>(grid, p, st);
+    case 256 * 8 + 4: return launch_norm_fwd_t<MX, 4, 256>(grid, p, st);
+    case 512 * 8 + 1: return launch_norm_fwd_t<MX, 1, 512>(grid, p, st);
+    case 512 * 8 + 3: return launch_norm_fwd_t<MX, 3, 512>(grid, p, st);
+    case 512 * 8 + 4: return launch_norm_fwd_t<MX, 4, 512>(grid, p, st);
+    case 1024 * 8 + 1: return launch_norm_fwd_t<MX, 1, 1024>(grid, p, st);
+    case 1024 * 8 + 2: return launch_norm_fwd_t<MX, 2, 1024>(grid, p, st);
+    case 1024 * 8 + 3: return launch_norm_fwd_t<MX, 3, 1024>(grid, p, st);
+    default: return launch_norm_fwd_t<MX, 4, 1024>(grid, p, st);
+  }
 }
 
-template <bool DG, int T>
-cudaError_t launch_norm_bwd_t(int V, unsigned grid, size_t smem, const NormBwdParams& p, cudaStream_t st) {
-  switch (V) {
-    case 1: return launch_pdl(qlora_norm_bwd_kernel<1, DG, T>, dim3(grid), dim3(T), smem, st, p);
-    case 2: return launch_pdl(qlora_norm_bwd_kernel<2, DG, T>, dim3(grid), dim3(T), smem, st, p);
-    case 3: return launch_pdl(qlora_norm_bwd_kernel<3, DG, T>, dim3(grid), dim3(T), smem, st, p);
-    default: return launch_pdl(qlora_norm_bwd_kernel<4, DG, T>, dim3(grid), dim3(T), smem, st, p);
-  }
+template <bool DG, int V, int T>
+cudaError_t launch_norm_bwd_t(unsigned grid, const NormBwdParams& p, cudaStream_t st) {
+  // the ring; with several groups of at most 2 vectors it is larger than their sums [groups - 1][K]
+  const size_t smem = size_t(norm::bwd_stages(V, T)) * norm::bwd_stage_bytes(V, T);
+  if (!set_smem(qlora_norm_bwd_kernel<V, DG, T>, smem)) return cudaErrorInvalidValue;
+  return launch_pdl(qlora_norm_bwd_kernel<V, DG, T>, dim3(grid), dim3(T), smem, st, p);
 }
 
 template <bool DG>
 cudaError_t launch_norm_bwd(const NormPlan& np, unsigned grid, const NormBwdParams& p, cudaStream_t st) {
-  const size_t smem = DG ? size_t(np.groups - 1) * size_t(p.K) * 4 : 0;   // at most 28 KB
-  if (np.threads == 256) return launch_norm_bwd_t<DG, 256>(np.V, grid, smem, p, st);
-  if (np.threads == 512) return launch_norm_bwd_t<DG, 512>(np.V, grid, smem, p, st);
-  return launch_norm_bwd_t<DG, 1024>(np.V, grid, smem, p, st);
+  switch (np.threads * 8 + np.V) {
+    case 256 * 8 + 1: return launch_norm_bwd_t<DG, 1, 256>(grid, p, st);
+    case 256 * 8 + 2: return launch_norm_bwd_t<DG, 2, 256>(grid, p, st);
+    case 512 * 8 + 1: return launch_norm_bwd_t<DG, 1, 512>(grid, p, st);
+    case 512 * 8 + 2: return launch_norm_bwd_t<DG, 2, 512>(grid, p, st);
+    case 1024 * 8 + 1: return launch_norm_bwd_t<DG, 1, 1024>(grid, p, st);
+    case 1024 * 8 + 2: return launch_norm_bwd_t<DG, 2, 1024>(grid, p, st);
+    case 1024 * 8 + 3: return launch_norm_bwd_t<DG, 3, 1024>(grid, p, st);
+    default: return launch_norm_bwd_t<DG, 4, 1024>(grid, p, st);
+  }
 }
 
-// CTAs of the backward kernel: every row has a group, at most `per_sm` CTAs per SM.  Each CTA
+// CTAs of the backward kernel: every row has a group, and no more than the SMs hold at once.  Each CTA
 // writes one partial row of dgamma, so the count also sizes the workspace.
 int64_t norm_bwd_ctas(const NormPlan& np, int64_t M, int sms) {
   const int64_t need = (M + np.groups - 1) / np.groups;
-  const int64_t most = int64_t(sms) * (np.threads > 512 ? 2 : 4);
+  const int64_t most = int64_t(sms) * norm::bwd_per_sm(np.threads);
   return need < most ? need : most;
 }
 
