@@ -311,7 +311,10 @@ qlora_status_t run_narrow(const qlora_weight_t* Wg, const qlora_weight_t* Wu, co
   const int64_t N = Wg->N, K = Wg->K;
   const int nw = Wu ? 2 : 1;
   const int nb = narrow_blocks(M);
-  qlora_status_t rc = narrow_down(Wg, Wu, X, Ag, Au, T, Zs, M, r, scale, st);
+  const int cols = Wu ? narrow::kRows / 2 : narrow::kRows;
+  const int64_t tiles = (N + cols - 1) / cols, chunks = (K + narrow::CK - 1) / narrow::CK, units = tiles * chunks;
+  if (units > INT32_MAX) return QLORA_ERR_UNSUPPORTED;
+  const qlora_status_t rc = narrow_down(Wg, Wu, X, Ag, Au, T, Zs, M, r, scale, st);
   if (rc != QLORA_OK) return rc;
   p.w[0] = narrow_weight(Wg, Bg);
   if (Wu) p.w[1] = narrow_weight(Wu, Bu);
@@ -326,19 +329,17 @@ qlora_status_t run_narrow(const qlora_weight_t* Wg, const qlora_weight_t* Wu, co
   p.K = int(K);
   p.r = r;
   p.ldzs = nw * r;
-  const int cols = Wu ? narrow::kRows / 2 : narrow::kRows;
-  p.tiles = int((N + cols - 1) / cols);
-  p.chunks = int((K + narrow::CK - 1) / narrow::CK);
+  p.tiles = int(tiles);
+  p.chunks = int(chunks);
   p.one = 1u;
   // Equal ranges of (tile, chunk) units over the SMs; without room for the partials, or with more
   // tiles than counters, whole tiles.
   p.status = ws_status(ws);
   p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + kCounterOffset);
   p.partial = partial;
-  const int64_t sms = num_sms(), units = int64_t(p.tiles) * p.chunks;
+  const int64_t sms = num_sms();
   const bool split = p.tiles <= narrow::kMaxCounters && partial_bytes >= narrow_partial_bytes(M, sms);
   const int64_t iters = split ? (units + sms - 1) / sms : (p.tiles + sms - 1) / sms * p.chunks;
-  if (units > INT32_MAX) return QLORA_ERR_UNSUPPORTED;
   p.iters = int(iters);
   const unsigned grid = unsigned((units + iters - 1) / iters);
   if (Wu)

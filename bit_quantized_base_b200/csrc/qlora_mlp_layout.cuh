@@ -5,9 +5,14 @@
 namespace qlora {
 namespace {
 
-// Work items a pair tile's contraction is split into (1: not).  A pair takes about 0.55 us for a step
-// of a 512-row tile and 0.33 us for one of at most 256 rows (measured); a split costs its fp32
-// accumulators, written and read once, and a launch.  `room`: bytes for the accumulators.
+// Work items a pair tile's contraction is split into (1: not).  A pair takes about 0.5 us for a step
+// of a 512-row tile and 0.35 us for one of at most 256 rows; a split costs its fp32 accumulators,
+// written and read once, and a launch.  Items for more than nine tenths of the pairs count as another
+// round: the last pairs wait for SMs that the kernel before still holds (128 x 2048, 14336 deep: 72
+// items 40 us, 64 items 32).  Measured on whole calls against the best of 1..16 items: within 4 % for
+// 33 x 2 x 2048 from 7168 (1: 72 us, best 4: 34), 1021 x 2048 from 8192 (119, best 3: 78), 300 x 4096
+// from 4096 (71, best 3: 33), 200 x 2 x 14336 from 4096 (best 1: 89; 2: 106).
+// `room`: bytes for the accumulators.
 struct SplitPlan {
   int S;
   size_t bytes;
@@ -16,12 +21,13 @@ SplitPlan split_plan(int64_t M, int64_t tiles, int64_t steps, int64_t width, int
   SplitPlan best{1, 0};
   if (M <= 0) return best;
   const int64_t pairs = sms / 2;
-  const double step_us = M > 256 ? 0.55 : 0.33;
+  const int64_t filled = pairs * 9 / 10;
+  const double step_us = M > 256 ? 0.5 : 0.35;
   double cost = double((tiles + pairs - 1) / pairs) * double(steps) * step_us;
   for (int S = 2; S <= 16 && steps / S >= 4; ++S) {
     const size_t bytes = size_t(S) * size_t(M) * size_t(width) * 4;
     if (bytes > room) break;
-    const double c = double((tiles * S + pairs - 1) / pairs) * double((steps + S - 1) / S) * step_us + 5.0 +
+    const double c = double((tiles * S + filled - 1) / filled) * double((steps + S - 1) / S) * step_us + 5.0 +
                      double(bytes) * 2 / 4.0e6;
     if (c < 0.95 * cost) {
       cost = c;
@@ -62,15 +68,14 @@ size_t act_down_sum_bytes(int64_t M, int64_t N, int nb, int r, int sms) {
   return size_t(rows > 0 ? rows : 0) * size_t(nb) * size_t(r) * 4;
 }
 
-// n = 2 (gated) or 1 weights.  header | Zs [M, n r] | T [n][M, r] | backward: U [n][M, r]
-// and the rest of its roundings [n][M, r], gradients of the pre-activations [n][M, N] bf16, the splits'
-// sums of U, bias partials
-// [ceil(M/128)][N] fp32 (n = 1), and the short-batch kernels' fp32 partials.
 // fp32 partials of the narrow kernel (batches of up to 16 rows): two pieces per CTA.
 size_t narrow_partial_bytes(int64_t M, int64_t sms) {
   return M > 0 && M <= narrow::kMaxRows ? size_t(sms) * 2 * narrow::partial_floats(int(M)) * 4 : 0;
 }
 
+// n = 2 (gated) or 1 weights.  header | Zs [M, n r] | T [n][M, r] | backward: U [n][M, r] and the rest
+// of its rounding [n][M, r], gradients of the pre-activations [n][M, N] bf16, the splits' fp32 sums of
+// U, bias partials [ceil(M/128)][N] fp32 (n = 1) | fp32 partials or accumulators of the product.
 struct MlpLayout {
   size_t zs, t, u, u_lo, grad, sums, bias, partial, total;
 };
