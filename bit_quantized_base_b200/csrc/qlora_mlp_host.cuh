@@ -279,7 +279,10 @@ qlora_status_t narrow_down(const qlora_weight_t* Wg, const qlora_weight_t* Wu, c
   d.r = r;
   d.nw = nw;
   d.ldzs = nw * r;
-  d.S = K >= 4096 ? 8 : (K >= 1024 ? 4 : 1);
+  // CTAs per row group: beside the narrow kernel, which wants every SM, half as many for one depth as
+  // beside the split one (one token of 2 x 14336 from 4096: 36 us with 8, 33 with 4)
+  const int64_t deep = M <= narrow::kMaxRows ? 2 : 1;
+  d.S = K >= 4096 * deep ? 8 : (K >= 1024 * deep ? 4 : 1);
   d.s = scale;
   const unsigned groups = unsigned((nw * r + 15) / 16);
   return nb == 1 ? launch_narrow_down_t<1>(d, groups, st) : launch_narrow_down_t<2>(d, groups, st);
