@@ -21,14 +21,19 @@ NormPlan norm_plan(int64_t K, int want) {
   return p;
 }
 
-// A short batch leaves SMs idle, so its rows are spread over as many threads as they fill (one
-// vector each: the fewest instructions between the load and the store); a long one keeps more
-// bytes in flight per thread.
-// The backward kernel holds two rows and the dgamma sums, so it stops at two.
-int norm_vectors(int64_t M, int sms, bool bwd) { return M <= 4 * int64_t(sms) ? 1 : (bwd ? 2 : 4); }
+// Vectors a thread should hold.  Groups of 1024 threads leave one CTA per SM, whose barriers stop all
+// its loads: they are for rows that nothing smaller holds.  Up to there fewer vectors shorten the way
+// from the load to the store, more of them keep more rows per SM in flight.  Measured, microseconds
+// with 1 / 2 / 4 vectors: forward 592 x 4096 6.6 / 5.1 / 5.1, 148 x 7168 3.6 / 2.8 / 2.8, 300 x 7168
+// 9.7 / 6.2 / 5.5, 300 x 1024 2.0 / 2.1 / 2.2; backward with 1 / 2 (it holds the dgamma sums as well
+// and stops there) 592 x 7168 13.3 / 9.9, 64 x 4096 2.9 / 2.4, 64 x 1024 2.1 / 2.4.
+int norm_vectors(int64_t M, int64_t K, int sms, bool bwd) {
+  if (K <= 2048 && M <= (bwd ? 2 : 4) * int64_t(sms)) return 1;
+  if (bwd) return 2;
+  return (K <= 4096 && M <= 4 * int64_t(sms)) || (K <= 8192 && M <= sms) ? 2 : 4;
+}
 
-// The (V, T) that norm_plan makes: more than two vectors a thread only in groups of more than want = 4
-// (forward) or 2 (backward) leaves, 512 threads with two only in the backward pass.
+// The (V, T) that norm_plan makes of those.
 template <bool MX, int V, int T>
 cudaError_t launch_norm_fwd_t(unsigned grid, const NormFwdParams& p, cudaStream_t st) {
   return launch_pdl(qlora_norm_fwd_kernel<V, MX, T>, dim3(grid), dim3(T), 0, st, p);
@@ -41,11 +46,9 @@ cudaError_t launch_norm_fwd(const NormPlan& np, unsigned grid, const NormFwdPara
     case 256 * 8 + 2: return launch_norm_fwd_t<MX, 2, 256>(grid, p, st);
     case 256 * 8 + 3: return launch_norm_fwd_t<MX, 3, 256>(grid, p, st);
     case 256 * 8 + 4: return launch_norm_fwd_t<MX, 4, 256>(grid, p, st);
-    case 512 * 8 + 1: return launch_norm_fwd_t<MX, 1, 512>(grid, p, st);
+    case 512 * 8 + 2: return launch_norm_fwd_t<MX, 2, 512>(grid, p, st);
     case 512 * 8 + 3: return launch_norm_fwd_t<MX, 3, 512>(grid, p, st);
     case 512 * 8 + 4: return launch_norm_fwd_t<MX, 4, 512>(grid, p, st);
-    case 1024 * 8 + 1: return launch_norm_fwd_t<MX, 1, 1024>(grid, p, st);
-    case 1024 * 8 + 2: return launch_norm_fwd_t<MX, 2, 1024>(grid, p, st);
     case 1024 * 8 + 3: return launch_norm_fwd_t<MX, 3, 1024>(grid, p, st);
     default: return launch_norm_fwd_t<MX, 4, 1024>(grid, p, st);
   }
@@ -64,9 +67,7 @@ cudaError_t launch_norm_bwd(const NormPlan& np, unsigned grid, const NormBwdPara
   switch (np.threads * 8 + np.V) {
     case 256 * 8 + 1: return launch_norm_bwd_t<DG, 1, 256>(grid, p, st);
     case 256 * 8 + 2: return launch_norm_bwd_t<DG, 2, 256>(grid, p, st);
-    case 512 * 8 + 1: return launch_norm_bwd_t<DG, 1, 512>(grid, p, st);
     case 512 * 8 + 2: return launch_norm_bwd_t<DG, 2, 512>(grid, p, st);
-    case 1024 * 8 + 1: return launch_norm_bwd_t<DG, 1, 1024>(grid, p, st);
     case 1024 * 8 + 2: return launch_norm_bwd_t<DG, 2, 1024>(grid, p, st);
     case 1024 * 8 + 3: return launch_norm_bwd_t<DG, 3, 1024>(grid, p, st);
     default: return launch_norm_bwd_t<DG, 4, 1024>(grid, p, st);
@@ -97,7 +98,7 @@ extern "C" {
 size_t qlora_rmsnorm_workspace_size(int64_t M, int64_t K) {
   if (check_norm(M, K, 0.0f) != QLORA_OK) return 0;
   const int sms = num_sms();
-  const NormPlan np = norm_plan(K, norm_vectors(M, sms, true));
+  const NormPlan np = norm_plan(K, norm_vectors(M, K, sms, true));
   const int64_t rows = norm_bwd_ctas(np, M, sms);
   return align_up(size_t(rows > 0 ? rows : 1) * size_t(K) * 4, 256);
 }
@@ -114,7 +115,7 @@ qlora_status_t qlora_rmsnorm_fwd(const void* X, const void* R, const void* gamma
     return QLORA_ERR_INVALID_ARG;
   if (M == 0) return QLORA_OK;
   if (!Y && !codes) return QLORA_ERR_INVALID_ARG;
-  const NormPlan np = norm_plan(K, norm_vectors(M, num_sms(), false));
+  const NormPlan np = norm_plan(K, norm_vectors(M, K, num_sms(), false));
   NormFwdParams p{};
   p.x = static_cast<const __nv_bfloat16*>(X);
   p.res = static_cast<const __nv_bfloat16*>(R);
@@ -146,7 +147,7 @@ qlora_status_t qlora_rmsnorm_bwd(const void* S, const float* rstd, const void* g
     return QLORA_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int sms = num_sms();
-  const NormPlan np = norm_plan(K, norm_vectors(M, sms, true));
+  const NormPlan np = norm_plan(K, norm_vectors(M, K, sms, true));
   const int64_t ctas = norm_bwd_ctas(np, M, sms);
   if (dgamma && (!ws || !aligned16(ws) || ws_bytes < size_t(ctas) * size_t(K) * 4))
     return QLORA_ERR_WORKSPACE;
