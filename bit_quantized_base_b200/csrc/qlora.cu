@@ -508,7 +508,7 @@ qlora_status_t launch_fused_t(const FusedParams& p, int grid, bool grouped, cuda
   const size_t smem = fused::smem_bytes(p.E);
   if (!set_smem(qlora_fused_gemm_kernel<FMT, DX>, smem)) return QLORA_ERR_CUDA;
   LaunchScope scope(grouped ? (DX ? kKindGFusedDx : kKindGFusedFwd) : (DX ? kKindFusedDx : kKindFusedFwd), st);
-  if (launch_pdl(qlora_fused_gemm_kernel<FMT, DX>, dim3(grid), dim3(fused::kThreads), smem, st, p) !=
+  if (launch_pdl(qlora_fused_gemm_kernel<FMT, DX>, dim3(grid), dim3(fused::threads()), smem, st, p) !=
       cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;

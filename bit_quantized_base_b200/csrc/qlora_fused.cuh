@@ -63,9 +63,13 @@
 //   Both (and kEpiAct's dX, which is the plain one otherwise) can split a tile's contraction over S
 //   work items, for batches whose tiles leave most CTA pairs idle: each item stores its fp32
 //   accumulator and qlora_split_kernel adds them in order and runs the epilogue.
-//   RB = 1 (at most 256 rows): one MMA block per tile; the room its second activation block leaves
-//   goes to a code ring of 16 stages, and scales are loaded four own steps ahead.  A step then takes
-//   half the tensor time, and with 4 code stages the memory's latency, not the decode, set the pace.
+//   RB = 1 (at most 256 rows): one MMA block per tile, half the tensor time per step; the room its
+//   second activation block leaves goes to a code ring of 16 stages (with 4, the memory's latency set the
+//   pace), scales are loaded four own steps ahead, and a third group of 4 warps decodes (a thread's
+//   decode is one dependent chain: 0.33 instructions per clock and scheduler with two groups).  33 rows
+//   of 2 x 2048 from 7168, whole call: 33.3 us with two groups, 30.3 with three, 32.8 with four (fewer
+//   registers).  A step still takes 0.55 us against 0.27 of tensor time.  Tried without gain: decoding
+//   before the operand stage is free (30.9), a ring of 8 stages for the activation rows that exist (32.7).
 #pragma once
 #include <cuda_bf16.h>
 #include "qlora_ptx.cuh"
@@ -83,8 +87,9 @@ constexpr int NS = 4, NC = 4;         // operand stages (activation blocks + wei
 constexpr int X_BYTES = HM * BK * 2;   // 16 KB per block
 constexpr int W_BYTES = HN * BK * 2;   // 16 KB
 constexpr int C_BYTES = HN * BK / 2;   // 4 KB of packed codes
-constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kCodeWarp = 6, kDqWarp0 = 7, kDqWarps = 8;
-constexpr int kThreads = (kDqWarp0 + kDqWarps) * 32;
+constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kCodeWarp = 6, kDqWarp0 = 7, kDqGroupWarps = 4;
+__host__ __device__ constexpr int dq_groups(int rb) { return rb == 1 ? 3 : 2; }
+__host__ __device__ constexpr int threads(int rb = MB) { return (kDqWarp0 + dq_groups(rb) * kDqGroupWarps) * 32; }
 constexpr int kTmemCols = 512;         // 2 blocks x 256 columns
 constexpr int GM = 8;                  // m-tiles per raster group
 // epilogue staging: per epilogue warp one tile of 32 rows x 32 output columns (bf16)
@@ -269,7 +274,7 @@ struct ItemGeom {
 };
 
 template <int FMT, bool DX, int EPI = kEpiPlain, bool SPLIT = false, int RB = fused::MB>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fused::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fused::threads(RB), 1)
 qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::type p) {
   using namespace fused;
   constexpr bool EX = EPI != kEpiPlain;
@@ -316,10 +321,10 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
     // stage full: leader = producer's expect-tx arrive + 4 dequant warps + 1 relayed arrive;
     // other CTA = its 4 dequant warps (waited on by its relay).  acc_empty is used in the leader.
     for (int s = 0; s < NS; ++s) {
-      ptx::mbar_init(full_s(s), rank == 0 ? 2 + kDqWarps / 2 : kDqWarps / 2);
+      ptx::mbar_init(full_s(s), rank == 0 ? 2 + kDqGroupWarps : kDqGroupWarps);
       ptx::mbar_init(empty_s(s), 1);
     }
-    for (int s = 0; s < NC; ++s) { ptx::mbar_init(full_c(s), 1); ptx::mbar_init(empty_c(s), kDqWarps / 2); }
+    for (int s = 0; s < NC; ++s) { ptx::mbar_init(full_c(s), 1); ptx::mbar_init(empty_c(s), kDqGroupWarps); }
     ptx::mbar_init(acc_full, 1);
     ptx::mbar_init(acc_empty, 2 * kEpiWarps);
     *abort_flag = 0;
@@ -656,11 +661,12 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
     }
   } else {
     // ------------------------------------------------------------------ dequant
+    constexpr int kGroups = dq_groups(RB);
     const int dw = warp - kDqWarp0;
     const int grp = dw >> 2;
     const int tg = (dw & 3) * 32 + lane;
     const ItemGeom<DX> geo(tg);
-    // Cursor over this group's steps (every other step of the CTA's pipeline): tile t (the lt-th
+    // Cursor over this group's steps (every kGroups-th step of the CTA's pipeline): tile t (the lt-th
     // of this pair), step ks of the tile (ks == nk is the LoRA step), weight-half origin h0.
     struct Cursor {
       int t, ks, kb, ke, h0, e;
@@ -715,12 +721,12 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       sc_q[k] = scale_for(pf);
-      advance(pf, 2);
+      advance(pf, kGroups);
     }
     while (cur.t < num_items) {
       const ItemScale s_pref = scale_for(pf);   // AHEAD own steps ahead
       const ItemScale s_cur = sc_q[0];
-      advance(pf, 2);
+      advance(pf, kGroups);
       const uint32_t i = cur.i;                                    // pipeline step
       const uint32_t sw = i % NS, pw = (i / NS) & 1u;
       const uint32_t rb = geo.op_row_base(ptx::smem_u32(wsm + sw * W_BYTES));
@@ -798,7 +804,7 @@ qlora_fused_gemm_kernel(const __grid_constant__ typename FusedParamsOf<EPI>::typ
 #pragma unroll
       for (int k = 0; k + 1 < AHEAD; ++k) sc_q[k] = sc_q[k + 1];
       sc_q[AHEAD - 1] = s_pref;
-      advance(cur, 2);
+      advance(cur, kGroups);
     }
   }
 

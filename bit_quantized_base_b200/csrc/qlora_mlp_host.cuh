@@ -16,7 +16,7 @@ qlora_status_t launch_fused_ex_s(const FusedExParams& p, int grid, bool early, c
   const size_t smem = fused::smem_bytes(1, RB);
   if (!set_smem(qlora_fused_gemm_kernel<FMT, DX, EPI, SPLIT, RB>, smem)) return QLORA_ERR_CUDA;
   LaunchScope scope(EPI == kEpiAct ? (DX ? kKindFusedDx : kKindActFwd) : (DX ? kKindGatedDx : kKindGatedFwd), st);
-  if (launch_pdl(qlora_fused_gemm_kernel<FMT, DX, EPI, SPLIT, RB>, dim3(grid), dim3(fused::kThreads), smem, st, p,
+  if (launch_pdl(qlora_fused_gemm_kernel<FMT, DX, EPI, SPLIT, RB>, dim3(grid), dim3(fused::threads(RB)), smem, st, p,
                  early) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
