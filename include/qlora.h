@@ -140,7 +140,9 @@ typedef enum {
  * most 256 rows the size includes the fp32 split partials of the short-batch kernels (tens of MB
  * for a 14336 x 4096 weight); a call whose workspace lacks room for them (e.g. one sized for
  * more than 256 rows, which need none) runs the tiled kernels instead: the same results up to
- * the order of fp32 additions.  The training calls reject only a workspace smaller than the
+ * the order of fp32 additions.  The gated MLP and the layer with an epilogue keep the partials of
+ * up to 16 rows, and the accumulators of contractions split over idle SMs (batches of few tiles), in
+ * the same optional part.  The training calls reject only a workspace smaller than the
  * part without those partials (QLORA_ERR_WORKSPACE). */
 QLORA_API size_t qlora_workspace_size(int op, const qlora_weight_t* W, int64_t M, int r, int E);
 

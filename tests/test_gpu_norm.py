@@ -290,3 +290,29 @@ def test_gain_gradient_without_epsilon_and_rstd(M, K):
     terms = f64(dY) * f64(S) * rstd[:, None]
     # binary32 sums of at most M terms, each with a few roundings of its own
     close(dg, terms.sum(axis=0), (M + 16) * 2.0 ** -24 * np.abs(terms).sum(axis=0), "dgamma")
+
+
+@pytest.mark.parametrize("M,K", [(64, 1024), (700, 1024), (40, 4096), (640, 8192), (3, 32768)])
+def test_mxfp8_products_over_a_wide_range(M, K):
+    """With codes wanted, Y is the definition's value rounded once, for rows and gains of any magnitude:
+    equal to the rounded binary64 value, but for values within 2^-40 of a border of two bf16 values."""
+    from bit_quantized_base_b200 import qlora as Q
+    rng = np.random.default_rng(M + K)
+    X = rng.standard_normal((M, K)) * 2.0 ** rng.integers(-50, 51, (M, 1)) * 2.0 ** rng.integers(-6, 7, (M, K))
+    X[rng.random((M, K)) < 0.01] = 0.0
+    g = rng.standard_normal(K) * 2.0 ** rng.integers(-20, 21, K)
+    X, g = (torch.from_numpy(t.astype(np.float32)).to(BF) for t in (X, g))
+    Y, R = torch.empty(M, K, dtype=BF, device="cuda"), torch.empty(M, dtype=torch.float32, device="cuda")
+    C, E = (torch.empty(M, k, dtype=torch.uint8, device="cuda") for k in (K, K // 32))
+    Q.qlora_rmsnorm_fwd(X.cuda(), None, g.cuda(), 0.0, None, Y, C, E, R, M, K)
+    C2, E2 = torch.empty_like(C), torch.empty_like(E)
+    Q.qlora_mxfp8_quantize(Y, M, K, C2, E2)
+    torch.cuda.synchronize()
+    x = f64(X)
+    ref = x / np.sqrt((x * x).mean(axis=1, keepdims=True)) * f64(g)[None, :]
+    m, e = np.frexp(ref)
+    frac = np.abs(m * 256.0 - np.floor(m * 256.0) - 0.5)
+    sure = (frac > 2.0 ** -32) & ((np.abs(ref) > 2.0 ** -100) | (ref == 0))
+    assert sure.mean() > 0.999
+    assert np.array_equal(f64(Y)[sure], round_bf16(ref)[sure])
+    assert torch.equal(C, C2) and torch.equal(E, E2)
