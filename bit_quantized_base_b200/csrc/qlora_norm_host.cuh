@@ -111,7 +111,7 @@ qlora_status_t qlora_rmsnorm_fwd(const void* X, const void* R, const void* gamma
   if (!act_ok(X, M) || !opt_ok(R) || !opt_ok(gamma) || !opt_ok(S) || !opt_ok(Y) || !opt_ok(codes) ||
       !opt_ok(scales) || !opt_ok(rstd))
     return QLORA_ERR_INVALID_ARG;
-  if ((codes == nullptr) != (scales == nullptr) || (S && !R) || (codes && K % 32 != 0))
+  if ((codes == nullptr) != (scales == nullptr) || (S && (!R || S == Y)) || (codes && K % 32 != 0))
     return QLORA_ERR_INVALID_ARG;
   if (M == 0) return QLORA_OK;
   if (!Y && !codes) return QLORA_ERR_INVALID_ARG;

@@ -266,7 +266,7 @@ QLORA_API qlora_status_t qlora_linear_fwd_w4a8_codes(const qlora_weight_t* W, co
  * that reads S sees the numbers the forward normalised.  R NULL: S is X itself.
  *   X, R [M,K] bf16 (R NULL or given); gamma [K] bf16 or NULL (all ones);
  *   S [M,K] bf16 out or NULL (only with R); may be the same buffer as X or R;
- *   Y [M,K] bf16 out or NULL; may be the same buffer as X or R (not as S);
+ *   Y [M,K] bf16 out or NULL; may be the same buffer as X or R (as S: refused);
  *   codes [M,K] uint8 and scales [M,K/32] uint8 out, both or neither: Y in MXFP8, bit for bit what
  *     qlora_mxfp8_quantize makes of Y (written or not) -- the input of qlora_linear_fwd_w4a8_codes;
  *   rstd [M] fp32 out or NULL, for the backward pass.  At least one of Y and codes is required.

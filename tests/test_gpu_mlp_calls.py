@@ -187,3 +187,31 @@ def test_a_larger_workspace_serves_the_gradients_of_fewer_rows(M):
     g.ok()
     for x, y in zip(want, got):
         assert_close(to_f64(y), to_f64(x), "gradient")
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in the widest tensors: the last rows are those of a call on them alone."""
+    from bit_quantized_base_b200 import qlora as Q
+    M, N, K, r, n, s = 140000, 16384, 64, 8, 300, 2.0
+    small = Gated("mxfp4", n, N, K, r, seed=6)
+    X = torch.randn(M, K, device="cuda").to(BF)
+    dH = torch.randn(M, N, dtype=BF, device="cuda")
+    H, G, U = (torch.empty(M, N, dtype=BF, device="cuda") for _ in range(3))
+    T, dX = torch.empty(2, M, r, dtype=BF, device="cuda"), nan(M, K)
+    outs = nan(r, K), nan(N, r), nan(r, K), nan(N, r)
+    ws = Q.alloc_workspace(Q.OP_GATED_MLP_BWD, small.Wg, M, r)
+    Q.qlora_gated_mlp_fwd(small.Wg, small.Wu, "silu", X, *small.ad, H, G, U, T, M, r, s, ws)
+    Q.qlora_gated_mlp_bwd(small.Wg, small.Wu, "silu", X, *small.ad, T, G, U, dH, dX, *outs, M, r, s, ws)
+    torch.cuda.synchronize()
+    assert Q.qlora_get_device_status(ws) == 0
+    x, dh, t = X[M - n:].clone(), dH[M - n:].clone(), T[:, M - n:].clone()
+    g, u = G[M - n:].clone(), U[M - n:].clone()
+    h2, g2, u2, t2, dx2 = nan(n, N), nan(n, N), nan(n, N), nan(2, n, r), nan(n, K)
+    Q.qlora_gated_mlp_fwd(small.Wg, small.Wu, "silu", x, *small.ad, h2, g2, u2, t2, n, r, s, small.ws)
+    Q.qlora_gated_mlp_bwd(small.Wg, small.Wu, "silu", x, *small.ad, t, g, u, dh, dx2, nan(r, K), nan(N, r),
+                          nan(r, K), nan(N, r), n, r, s, small.ws)
+    small.ok()
+    for name, a, b in (("H", H[M - n:], h2), ("G", g, g2), ("U", u, u2), ("T", t, t2), ("dX", dX[M - n:], dx2)):
+        assert_close(to_f64(a), to_f64(b), name)
+    for o in outs:
+        assert torch.isfinite(o.float()).all()

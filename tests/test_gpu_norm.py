@@ -316,3 +316,22 @@ def test_mxfp8_products_over_a_wide_range(M, K):
     assert sure.mean() > 0.999
     assert np.array_equal(f64(Y)[sure], round_bf16(ref)[sure])
     assert torch.equal(C, C2) and torch.equal(E, E2)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows are those of a call on them alone."""
+    from bit_quantized_base_b200 import qlora as Q
+    M, K, n = 66000, 32768, 16
+    X = torch.randn(M, K, dtype=BF, device="cuda")
+    g = torch.randn(K, device="cuda").to(BF)
+    rstd = torch.empty(M, dtype=torch.float32, device="cuda")
+    Y, dS = torch.empty_like(X), torch.empty_like(X)
+    Q.qlora_rmsnorm_fwd(X, None, g, EPS, None, Y, None, None, rstd, M, K)
+    Q.qlora_rmsnorm_bwd(X, rstd, g, EPS, Y, X, dS, None, M, K, None)
+    x = X[M - n:].clone()
+    y, ds, rs = torch.empty_like(x), torch.empty_like(x), torch.empty(n, dtype=torch.float32, device="cuda")
+    Q.qlora_rmsnorm_fwd(x, None, g, EPS, None, y, None, None, rs, n, K)
+    Q.qlora_rmsnorm_bwd(x, rs, g, EPS, y, x, ds, None, n, K, None)
+    torch.cuda.synchronize()
+    for a, b in ((Y[M - n:], y), (dS[M - n:], ds), (rstd[M - n:], rs)):
+        assert torch.equal(a, b)

@@ -81,3 +81,10 @@ def test_w4a8_codes(Q):
     assert call(0x70004, 0x80000) == "QLORA_ERR_INVALID_ARG"
     assert call(0x70000, 0x80000, ws=None) == "QLORA_ERR_WORKSPACE"
     assert call(None, None, M=0) == "QLORA_OK"
+
+
+def test_sum_and_output_in_one_buffer(Q):
+    a = dict(FWD, R=0x30000, S=0x20000)                      # S is Y's buffer
+    rc = Q.lib.qlora_rmsnorm_fwd(a["X"], a["R"], a["gamma"], a["eps"], a["S"], a["Y"], a["codes"], a["scales"],
+                                 a["rstd"], a["M"], a["K"], None)
+    assert Q.STATUS[rc] == "QLORA_ERR_INVALID_ARG"
