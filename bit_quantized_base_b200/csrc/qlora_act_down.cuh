@@ -11,6 +11,11 @@
 // U leaves as the sum of two bf16 tensors, its rounded value and the rest: dA = s U^T X multiplies both
 // (qlora_lora_wgrad_kernel<true>), so that the roundings of dA are the gradient's and its own.
 //
+// Batches of one row tile (LO): the gradients too enter U in two bf16 terms, the second from operand tiles
+// of its own.  U of a few rows is so few values that a rounding of dU is not averaged out: dA of one row
+// and rank 8 was off by up to 1.9 times its own rounding.  More rows have thousands of values, whose
+// error the square root of two bounds, and are not latency bound.
+//
 // Work split: 128-row tiles, the N columns of a tile over S CTAs (about two per SM in all, at least
 // two 64-column chunks each); every CTA writes its binary32 sums to the workspace and
 // qlora_down_sum_kernel adds them in split order.  (Clusters of CTAs adding through distributed
@@ -35,9 +40,9 @@ constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kRowStep = kWarps * 4;            // rows between two vectors of a thread
 constexpr int kTmemCols = 128;                  // accumulator of stream b at column 64 b
 constexpr int kVec = BM * BK / 8 / kThreads;    // 16-byte vectors a thread holds per tensor
-// two stages of operand tiles and rows of B, barriers, bias partials
-__host__ __device__ constexpr size_t smem_bytes(int nb) {
-  return 1024 + size_t(2 * nb) * (T_BYTES + R_BYTES) + 256 + kWarps * 256;
+// two stages of operand tiles (lo: and as many of their roundings) and rows of B, barriers, bias partials
+__host__ __device__ constexpr size_t smem_bytes(int nb, bool lo) {
+  return 1024 + size_t(2 * nb) * ((lo ? 2 : 1) * T_BYTES + R_BYTES) + 256 + kWarps * 256;
 }
 
 }  // namespace actdown
@@ -53,14 +58,15 @@ struct ActDownParams {
   int M, N, r, rpad, num_k, S, sps;
 };
 
-template <int NB, int ACT>
-__global__ void __launch_bounds__(actdown::kThreads, 2)
+template <int NB, int ACT, bool LO>
+__global__ void __launch_bounds__(actdown::kThreads, LO ? 1 : 2)
 qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
   using namespace actdown;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* tail = smem + size_t(2 * NB) * (T_BYTES + R_BYTES);
+  constexpr int NT = LO ? 2 * NB : NB;           // operand tiles of a stage: NB, then their roundings
+  uint8_t* tail = smem + size_t(2 * NT) * T_BYTES + size_t(2 * NB) * R_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(tail);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -71,9 +77,9 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
   auto empty = [&](uint32_t q) { return b0 + 16u + 8u * q; };
   auto b_full = [&](uint32_t q) { return b0 + 32u + 8u * q; };
   const uint32_t acc_full = b0 + 48u;
-  auto tile = [&](uint32_t q, int b) { return ptx::smem_u32(smem) + (q * NB + uint32_t(b)) * uint32_t(T_BYTES); };
+  auto tile = [&](uint32_t q, int b) { return ptx::smem_u32(smem) + (q * NT + uint32_t(b)) * uint32_t(T_BYTES); };
   auto rtile = [&](uint32_t q, int b) {
-    return ptx::smem_u32(smem) + uint32_t(2 * NB * T_BYTES) + (q * NB + uint32_t(b)) * uint32_t(R_BYTES);
+    return ptx::smem_u32(smem) + uint32_t(2 * NT * T_BYTES) + (q * NB + uint32_t(b)) * uint32_t(R_BYTES);
   };
 
   const int mt = int(blockIdx.x) / p.S, split = int(blockIdx.x) % p.S;
@@ -123,6 +129,9 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
         const uint64_t ad = ptx::smem_desc(tile(q, b) + kk * 32, 16, 1024, ptx::kSw128);
         const uint64_t bd = ptx::smem_desc(rtile(q, b) + kk * 16 * rowb, 64 * rowb, 8 * rowb, rsw);
         ptx::mma_bf16(tmem + uint32_t(b) * 64u, ad, bd, idesc, (n > 0 || kk > 0) ? 1u : 0u);
+        if constexpr (LO)
+          ptx::mma_bf16(tmem + uint32_t(b) * 64u, ptx::smem_desc(tile(q, NB + b) + kk * 32, 16, 1024, ptx::kSw128),
+                        bd, idesc, 1u);
       }
     ptx::mma_commit(empty(q));
   };
@@ -172,6 +181,10 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
         uint32_t wu[4] = {0u, 0u, 0u, 0u};
         if constexpr (NB == 2) { wu[0] = u[i].x; wu[1] = u[i].y; wu[2] = u[i].z; wu[3] = u[i].w; }
         uint32_t hi[NB][4], out1[4];
+        [[maybe_unused]] uint32_t lo[NB][4];
+        auto rest = [](float x0, float x1, uint32_t h) {   // what the rounding to h left
+          return ptx::cvt_bf16x2(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xFFFF0000u));
+        };
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float x0, x1, y0, y1;
@@ -181,8 +194,10 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
                     __uint_as_float(wu[j] & 0xFFFF0000u), x1, y1);
           if constexpr (NB == 1) { bsum[2 * j] += x0; bsum[2 * j + 1] += x1; }
           hi[0][j] = ptx::cvt_bf16x2(x0, x1);
+          if constexpr (LO) lo[0][j] = rest(x0, x1, hi[0][j]);
           if constexpr (NB == 2) {
             hi[1][j] = ptx::cvt_bf16x2(y0, y1);
+            if constexpr (LO) lo[1][j] = rest(y0, y1, hi[1][j]);
             out1[j] = p.ts1 ? ptx::cvt_bf16x2(y0 * up_ratio, y1 * up_ratio) : hi[1][j];
           }
         }
@@ -192,6 +207,7 @@ qlora_act_down_kernel(const __grid_constant__ ActDownParams p) {
 #pragma unroll
         for (int b = 0; b < NB && stage_ok; ++b) {
           ptx::st_shared_v4(tile(q, b) + off, hi[b][0], hi[b][1], hi[b][2], hi[b][3]);
+          if constexpr (LO) ptx::st_shared_v4(tile(q, NB + b) + off, lo[b][0], lo[b][1], lo[b][2], lo[b][3]);
         }
         if (row < p.M && col < p.N) {
           const size_t o = size_t(row) * p.N + col;

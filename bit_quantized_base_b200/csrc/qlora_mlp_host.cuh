@@ -115,14 +115,22 @@ qlora_status_t launch_split(const FusedExParams& p, int n, bool gated, cudaStrea
   return QLORA_OK;
 }
 
+template <int NB, int ACT, bool LO>
+qlora_status_t launch_act_down_lo(const ActDownParams& p, unsigned grid, cudaStream_t st) {
+  const size_t smem = actdown::smem_bytes(NB, LO);
+  auto kern = qlora_act_down_kernel<NB, ACT, LO>;
+  if (!set_smem(kern, smem)) return QLORA_ERR_CUDA;
+  LaunchScope scope(kKindActDown, st);
+  if (launch_pdl(kern, dim3(grid), dim3(actdown::kThreads), smem, st, p) != cudaSuccess) return QLORA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+// dZ of no activation is dY itself: no rounding.
 template <int NB, int ACT>
 qlora_status_t launch_act_down_t(const ActDownParams& p, unsigned grid, cudaStream_t st) {
-  const size_t smem = actdown::smem_bytes(NB);
-  if (!set_smem(qlora_act_down_kernel<NB, ACT>, smem)) return QLORA_ERR_CUDA;
-  LaunchScope scope(kKindActDown, st);
-  if (launch_pdl(qlora_act_down_kernel<NB, ACT>, dim3(grid), dim3(actdown::kThreads), smem, st, p) != cudaSuccess)
-    return QLORA_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  if constexpr (NB == 2 || ACT != act::kNone) {
+    if (p.M <= actdown::BM) return launch_act_down_lo<NB, ACT, true>(p, grid, st);
+  }
+  return launch_act_down_lo<NB, ACT, false>(p, grid, st);
 }
 
 // Gradients of the pre-activations and their projections (nb = 1 or 2 streams): grad, U as u + u_lo, Zs.
@@ -192,8 +200,8 @@ qlora_status_t launch_act_down(int nb, int act, const void* dy, const void* a0, 
 
 // Up to this many rows the adapter gradients run ahead of dX on the same stream: a few microseconds,
 // after which dX may be launched early (its predecessor has waited for the gradients it reads), and
-// no events.  Longer batches run them beside dX.  Measured: gated, 77 rows of 2048 x 512, 44 us ahead
-// and 48 beside; 1021 rows of 8192 x 2048, 87 ahead and 82 beside.
+// no events.  Longer batches run them beside dX.  Measured: gated, 77 rows of 2 x 2048 from 7168, 44 us ahead
+// and 48 beside; one weight, 1021 rows of 8192 x 2048, 87 ahead and 78 beside.
 constexpr int64_t kWgradFirstRows = 256;
 
 // Runs `side_work` on the device's side stream beside `main_work` on `s`, joined into `s` again.  The

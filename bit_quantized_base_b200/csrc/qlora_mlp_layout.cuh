@@ -47,8 +47,8 @@ SplitPlan split_dx(int64_t N, int64_t K, int64_t M, int r, int n, int sms, size_
                     sms, room);
 }
 
-// The plan of the act_down kernel: S CTAs a 128-row tile, about two CTAs per SM in all, at least two
-// 64-column chunks each.
+// The plan of the act_down kernel: S CTAs a 128-row tile, about two CTAs per SM in all (one for a
+// single row tile, whose CTAs hold twice the operand tiles), at least two 64-column chunks each.
 struct ActDownPlan {
   int tiles, S, sps, num_k;
 };
@@ -56,7 +56,7 @@ ActDownPlan act_down_plan(int64_t M, int64_t N, int sms) {
   ActDownPlan p{};
   p.tiles = int((M + 127) / 128);
   p.num_k = int((N + 63) / 64);
-  const int most = std::max(1, std::min(p.tiles > 0 ? 2 * sms / p.tiles : 1, p.num_k / 2));
+  const int most = std::max(1, std::min(p.tiles > 1 ? 2 * sms / p.tiles : sms, p.num_k / 2));
   p.sps = (p.num_k + most - 1) / most;
   p.S = (p.num_k + p.sps - 1) / p.sps;                          // no split is empty
   return p;

@@ -320,8 +320,9 @@ QLORA_API qlora_status_t qlora_gated_mlp_fwd(const qlora_weight_t* Wg, const qlo
  * saved bf16 G and U):
  *   dX = dG deq(Wg) + dU deq(Wu) + s (dG Bg) Ag + s (dU Bu) Au
  *   dAg = s (dG Bg)^T X    dBg = s dG^T Tg    dAu = s (dU Bu)^T X    dBu = s dU^T Tu
- * dG and dU are rounded to bf16 as operands of every product; the rank-r products dG Bg and dU Bu
- * enter dAg and dAu in two bf16 terms (2^-17), dX in one.
+ * dG and dU are rounded to bf16 as operands of every product (up to 128 rows: taken in two bf16 terms,
+ * 2^-17, in dG Bg and dU Bu); the rank-r products dG Bg and dU Bu enter dAg and dAu in two terms,
+ * dX in one.
  *   T [2,M,r]: the forward's T_save, or NULL to recompute it from X, Ag and Au;
  *   G, U [M,N]: the forward's; dH [M,N]; dX [M,K] out or NULL; dAg, dAu [r,K], dBg, dBu [N,r] out;
  *   ws >= qlora_workspace_size(QLORA_OP_GATED_MLP_BWD, ...): holds dG and dU, 4 M N bytes.
@@ -352,8 +353,8 @@ QLORA_API qlora_status_t qlora_linear_act_fwd(const qlora_weight_t* W, const voi
 
 /* Backward of qlora_linear_act_fwd.  With dZ = dY act'(Z):
  *   dX = dZ deq(W) + s (dZ B) A    dA = s (dZ B)^T X    dB = s dZ^T T    dbias[n] = sum_m dZ[m,n]
- * (the residual's gradient is dY itself).  dZ is rounded to bf16 as the operand of the products, not
- * for dbias; dZ B enters dA in two bf16 terms.
+ * (the residual's gradient is dY itself).  dZ is rounded to bf16 as the operand of the products (up to
+ * 128 rows: taken in two bf16 terms in dZ B), not for dbias; dZ B enters dA in two bf16 terms.
  *   T [M,r] or NULL (recomputed); Z [M,N]: the forward's Z_save, may be NULL for act NONE;
  *   dX [M,K] out or NULL; dA [r,K], dB [N,r] out; dbias [N] bf16 out or NULL;
  *   ws >= qlora_workspace_size(QLORA_OP_ACT_BWD, W, M, r, 0).
